@@ -377,6 +377,133 @@ wkv7_status wkv7_gdn_bwd(const void* q, const void* k, const void* v, const void
                          void* stream);
 
 /*
+ * wkv7_la_fwd -- linear attention with one decay per head over whole sequences (no delta
+ * rule; the pages list operators of this family, this one is not among them):
+ *
+ *     S_t = e^{g_t} S_{t-1} + k_t v_t^T,     o_t = scale S_t^T q_t
+ *
+ * and a token whose mask is 0 leaves the state as it is (whatever k, v and g hold there) and
+ * reads it: o_t = scale S_{t-1}^T q_t.
+ *
+ *   q, k           [B, T, H, K]  dtype
+ *   v              [B, T, H, V]  dtype
+ *   g              [B, T, H]     dtype   log decay of each token and head, or
+ *                  [H]           dtype   of each head (g_per_head = 1); needs only element
+ *                                        alignment.  -inf resets the state.
+ *   s0             [N, H, K, V]  fp32    initial states, or NULL for zeros
+ *   mask           [B, T]        uint8   as for wkv7_fwd, or NULL
+ *   o              [B, T, H, V]  dtype   output (must not alias an input)
+ *   sT             [N, H, K, V]  fp32    final states, or NULL to skip; may equal s0
+ *   cu_seqlens, N, layout, algo          as for wkv7_fwd; a sequence may be empty.  If an
+ *                                        entry is out of order or range the whole call is
+ *                                        skipped (WKV7_ERR_DEVICE_BAD_SEQLENS); rows behind
+ *                                        the last sequence are left as they are.
+ *   scale                                any finite number
+ *   workspace      at least wkv7_la_fwd_workspace_bytes(..) bytes, 16-byte aligned (NULL
+ *                  when that is 0): start states of the segments that long sequences are
+ *                  cut into when there are few (sequence, head) pairs.  Calls that may
+ *                  overlap need workspaces of their own.
+ *
+ * K == V in {64, 128, 256}.  WKV7_ALGO_CHUNKED: bf16, head sizes 64 and 128, 128-token
+ * chunks on tcgen05 tensor cores: scores and states enter its products in bf16, sums, decays
+ * and the carried state are fp32 (the state update's operand in two bf16 parts, so sT is as
+ * good as fp32's).  Decays need no bound.  WKV7_ALGO_RECURRENT: fp32 on CUDA cores, every
+ * type and head size.  AUTO takes the chunked form where it exists.
+ */
+size_t wkv7_la_fwd_workspace_bytes(int B, int T, int H, int K, int V, int N, int packed,
+                                   wkv7_dtype dtype, wkv7_algo algo);
+
+wkv7_status wkv7_la_fwd(const void* q, const void* k, const void* v, const void* g, int g_per_head,
+                        const float* s0, const uint8_t* mask, void* o, float* sT, int B, int T,
+                        int H, int K, int V, const int32_t* cu_seqlens, int N, float scale,
+                        wkv7_layout layout, wkv7_dtype dtype, wkv7_algo algo, void* workspace,
+                        size_t workspace_bytes, void* stream);
+
+/*
+ * wkv7_la_step -- one decode token of the same recurrence for B independent states.
+ *
+ *   q, k           [B, H, K]     dtype
+ *   v              [B, H, V]     dtype
+ *   g              [B, H] or, g_per_head = 1, [H]  dtype
+ *   state          [B, H, K, V]  fp32    read
+ *   out_state      [B, H, K, V]  fp32    the new state; may equal state (no other overlap)
+ *   o              [B, H, V]     dtype   output (must not alias)
+ */
+wkv7_status wkv7_la_step(const void* q, const void* k, const void* v, const void* g, int g_per_head,
+                         const float* state, float* out_state, void* o, int B, int H, int K, int V,
+                         float scale, wkv7_dtype dtype, void* stream);
+
+/*
+ * wkv7_la_bwd -- backward of wkv7_la_fwd for L = sum(o * dout) + sum(S_T * dsT).  With
+ * G_t = dL/dS_t:
+ *
+ *     G_t = scale q_t do_t^T + e^{g_{t+1}} G_{t+1},   dq_t = scale S_t do_t,
+ *     dk_t = G_t v_t,   dv_t = G_t^T k_t,   dg_t = e^{g_t} <G_t, S_{t-1}>,
+ *
+ * ds0 = e^{g_0} G_0; a masked token passes G through and has dk = dv = dg = 0.
+ *
+ *   q, k, v, g, g_per_head, s0, mask, cu_seqlens, N, scale, layout, dtype, algo   as for
+ *                  wkv7_la_fwd
+ *   dout           shaped like v dtype   dL/do
+ *   dsT            [N, H, K, V]  fp32    dL/dS_T, or NULL for zero
+ *   dq, dk, dv     shaped like q, k, v   dtype   (must not alias an input or each other)
+ *   dg             shaped like g dtype   ([H]: summed over batch and tokens, in a fixed
+ *                                        order), or NULL to skip
+ *   ds0            [N, H, K, V]  fp32    or NULL to skip; must not alias s0 or dsT
+ *   workspace      at least wkv7_la_bwd_workspace_bytes(..) bytes, 16-byte aligned; calls
+ *                  that may overlap need workspaces of their own
+ *
+ * The results do not depend on scheduling (no atomic sums).
+ */
+size_t wkv7_la_bwd_workspace_bytes(int B, int T, int H, int K, int V, int N, int packed,
+                                   wkv7_dtype dtype, wkv7_algo algo);
+
+wkv7_status wkv7_la_bwd(const void* q, const void* k, const void* v, const void* g, int g_per_head,
+                        const float* s0, const uint8_t* mask, const void* dout, const float* dsT,
+                        void* dq, void* dk, void* dv, void* dg, float* ds0, int B, int T, int H,
+                        int K, int V, const int32_t* cu_seqlens, int N, float scale,
+                        wkv7_layout layout, wkv7_dtype dtype, wkv7_algo algo, void* workspace,
+                        size_t workspace_bytes, void* stream);
+
+/*
+ * wkv7_ln_fwd -- layer norm of `rows` rows of D elements:
+ *     y = (x - mean) rstd w + b,   rstd = (mean of (x - mean)^2 + eps)^-1/2.
+ * With groups > 1 row r uses weights and bias of group (r / inner) % groups: the norm of each
+ * head of a mixing layer's output o, [B, T, H, V] (groups = H, inner = 1) or head-first
+ * [B, H, T, V] (groups = H, inner = T).  rows must be a multiple of groups * inner.
+ *
+ *   x, y           [rows, D]     dtype   (y must not alias another tensor)
+ *   weight, bias   [groups, D]   wdtype  or NULL (1 and 0); bf16 x takes bf16 or fp32
+ *                                        weights, fp32 x fp32 ones
+ *   mean, rstd     [rows]        fp32    the statistics that wkv7_ln_bwd takes, or NULL
+ *   eps                                  finite, >= 0
+ *
+ * 1 <= D <= 32768, statistics in fp32 around the mean.
+ */
+wkv7_status wkv7_ln_fwd(const void* x, const void* weight, const void* bias, void* y, float* mean,
+                        float* rstd, int64_t rows, int groups, int64_t inner, int D, float eps,
+                        wkv7_dtype dtype, wkv7_dtype wdtype, void* stream);
+
+/*
+ * wkv7_ln_bwd -- gradients of wkv7_ln_fwd for L = sum(y * dy), from the forward's mean and
+ * rstd:  u = dy w,  xh = (x - mean) rstd,
+ *     dx = rstd (u - mean of u - xh * mean of (u xh)),
+ *     dweight = sum over the group's rows of dy xh,   dbias = sum of dy.
+ *
+ *   dx             [rows, D]     dtype   (must not alias another tensor)
+ *   dweight, dbias [groups, D]   wdtype  or NULL to skip; summed in fp32 in a fixed order
+ *   workspace      at least wkv7_ln_bwd_workspace_bytes(..) bytes, 16-byte aligned, when
+ *                  dweight or dbias is asked for
+ */
+size_t wkv7_ln_bwd_workspace_bytes(int64_t rows, int groups, int64_t inner, int D,
+                                   wkv7_dtype dtype);
+
+wkv7_status wkv7_ln_bwd(const void* x, const void* dy, const float* mean, const float* rstd,
+                        const void* weight, void* dx, void* dweight, void* dbias, int64_t rows,
+                        int groups, int64_t inner, int D, wkv7_dtype dtype, wkv7_dtype wdtype,
+                        void* workspace, size_t workspace_bytes, void* stream);
+
+/*
  * wkv7_get_last_error -- synchronises `stream`, returns and clears the sticky
  * device-side flag (WKV7_ERR_DEVICE_TIMEOUT / WKV7_ERR_DEVICE_BAD_SEQLENS) of
  * the current device, or WKV7_ERR_CUDA if the stream reports a CUDA error,

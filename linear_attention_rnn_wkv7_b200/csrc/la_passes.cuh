@@ -1,0 +1,239 @@
+// la_passes.cuh -- host side of the decay linear attention: how a problem is cut into
+// segments, the workspace, and the passes of the forward and the backward (la_common.cuh).
+#pragma once
+#include <algorithm>
+
+#include "la_common.cuh"
+#include "la_recurrent.cuh"
+
+namespace wkv7 {
+namespace la {
+
+struct Problem {
+    Geom geom;
+    int B, D;
+    bool bf16, chunked;
+    long long rows() const { return (long long)B * geom.T * geom.H; }
+    // spacing of the states kept for dg
+    int ck_every() const { return chunked ? kChunk : kRecChunk; }
+    // column slabs that one (segment, head) is split into
+    int slabs() const { return chunked ? 1 : D / 64; }
+};
+
+// Segments.  One segment per sequence needs nothing extra.  With fewer (sequence, head)
+// units than the GPU holds blocks, sequences are cut: a pass over y and z first gives every
+// segment's own state (half of a pass's reads, no outputs), la_chain_kernel joins them, and
+// all segments run at once.  The estimate below counts chunks on the longest block; the
+// extra launches and the join are charged as about three chunks.
+struct Plan {
+    int seg;
+    bool split;
+};
+inline Plan make_plan(const Problem& p) {
+    const Geom& g = p.geom;
+    // blocks that run at once: one per SM (tensor cores) or by registers (64 a state tile)
+    const long long resident = p.chunked ? 148 : 148LL * 384 / p.D;
+    const long long chunks = std::max<long long>(1, ((long long)g.T + kChunk - 1) / kChunk);
+    Plan best{(int)(chunks * kChunk), false};
+    if ((long long)chunks * kChunk > 0x7fffff80LL) best.seg = 0x7fffff80;
+    if (chunks < 4) return best;
+    if (g.cu) {
+        // lengths are on the device: cut only sequences longer than an even share
+        const long long share = chunks * g.H * p.slabs() / resident;
+        const long long c = std::max<long long>(4, share);
+        if (c < chunks) best = Plan{(int)(c * kChunk), true};
+        return best;
+    }
+    const long long units = (long long)g.N * g.H * p.slabs();
+    // (cut only for a gain beyond the estimate's own error)
+    double least = 0.85 * (double)((units + resident - 1) / resident) * (double)chunks;
+    for (long long n = 2; n <= std::min<long long>(chunks, 256); ++n) {
+        const long long c = (chunks + n - 1) / n, used = (chunks + c - 1) / c;
+        const long long waves = (units * used + resident - 1) / resident;
+        const double t = (double)(waves * c) * (1.0 + 0.5 * (double)(used - 1) / (double)used) + 3.0;
+        if (used > 1 && t < least) {
+            least = t;
+            best = Plan{(int)(c * kChunk), true};
+        }
+    }
+    return best;
+}
+
+// Workspace pieces, in floats, each rounded up to 256 bytes.
+struct Carve {
+    size_t at = 0;
+    size_t take(size_t bytes) {
+        const size_t here = at;
+        at += (bytes + 255) & ~(size_t)255;
+        return here;
+    }
+};
+struct Segs {
+    size_t state = 0, decay = 0;
+};
+inline Segs carve_segs(Carve& c, const Problem& p, const Plan& plan) {
+    Segs s;
+    if (!plan.split) return s;
+    const size_t n = (size_t)p.geom.slots(plan.seg) * p.geom.H;
+    s.state = c.take(n * p.D * p.D * sizeof(float));
+    s.decay = c.take(n * sizeof(float));
+    return s;
+}
+struct BwdSpace {
+    Segs fwd, rev;
+    size_t qdq, kdk, ck, ends, part, bytes;
+};
+inline BwdSpace carve_bwd(const Problem& p, const Plan& plan) {
+    Carve c;
+    BwdSpace b;
+    b.fwd = carve_segs(c, p, plan);
+    b.rev = carve_segs(c, p, plan);
+    const size_t dots = (size_t)p.rows() * p.slabs() * sizeof(float);
+    const size_t units = (size_t)p.geom.slots(p.ck_every()) * p.geom.H;
+    b.qdq = c.take(dots);
+    b.kdk = c.take(dots);
+    b.ck = c.take(units * p.D * p.D * sizeof(float));
+    b.ends = c.take(units * p.slabs() * sizeof(float));
+    b.part = c.take(units * sizeof(float));
+    b.bytes = c.at;
+    return b;
+}
+inline size_t fwd_workspace(const Problem& p) {
+    Carve c;
+    (void)carve_segs(c, p, make_plan(p));
+    return c.at;
+}
+inline size_t bwd_workspace(const Problem& p) { return carve_bwd(p, make_plan(p)).bytes; }
+
+template <typename Tin, bool kRev, bool kStateOnly>
+inline cudaError_t run_pass(const Pass<Tin>& a, const Problem& p, cudaStream_t stream) {
+    return launch_recurrent_pass<Tin, kRev, kStateOnly>(a, p.D, stream);
+}
+
+// The states before every segment, from y, z and the states before the first token.
+template <typename Tin, bool kRev>
+inline cudaError_t run_segments(Pass<Tin> a, const Problem& p, const float* init, uint8_t* ws,
+                                const Segs& s, cudaStream_t stream) {
+    a.seg_state = reinterpret_cast<float*>(ws + s.state);
+    a.seg_decay = reinterpret_cast<float*>(ws + s.decay);
+    if (const cudaError_t e = run_pass<Tin, kRev, true>(a, p, stream); e != cudaSuccess) return e;
+    const long long n = (long long)p.geom.N * p.geom.H * (p.D * p.D / 4);
+    if ((n + 255) / 256 > 0x7fffffffLL) return cudaErrorInvalidValue;
+    la_chain_kernel<kRev><<<(unsigned)((n + 255) / 256), 256, 0, stream>>>(
+        p.geom, init, a.seg_state, a.seg_decay, a.seg, p.D * p.D);
+    return cudaGetLastError();
+}
+
+template <typename Tin>
+inline cudaError_t forward(const Problem& p, const Tin* q, const Tin* k, const Tin* v, const Tin* g,
+                           int g_per_head, const float* s0, const uint8_t* mask, Tin* o, float* sT,
+                           float scale, uint8_t* ws, cudaStream_t stream) {
+    const Plan plan = make_plan(p);
+    Carve c;
+    const Segs s = carve_segs(c, p, plan);
+    Pass<Tin> a{};
+    a.geom = p.geom;
+    a.x = q;
+    a.y = k;
+    a.z = v;
+    a.g = g;
+    a.g_per_head = g_per_head;
+    a.mask = mask;
+    a.out = o;
+    a.pair_scale = a.inter_scale = scale;
+    a.key_scale = 1.f;
+    a.seg = plan.seg;
+    a.init = s0;
+    a.fin = sT;
+    if (plan.split) {
+        if (const cudaError_t e = run_segments<Tin, false>(a, p, s0, ws, s, stream);
+            e != cudaSuccess)
+            return e;
+        a.init = reinterpret_cast<float*>(ws + s.state);
+        a.init_by_slot = 1;
+    }
+    return run_pass<Tin, false, false>(a, p, stream);
+}
+
+template <typename Tin>
+inline cudaError_t backward(const Problem& p, const Tin* q, const Tin* k, const Tin* v,
+                            const Tin* g, int g_per_head, const float* s0, const uint8_t* mask,
+                            const Tin* dout, const float* dsT, Tin* dq, Tin* dk, Tin* dv, Tin* dg,
+                            float* ds0, float scale, uint8_t* ws, cudaStream_t stream) {
+    const Plan plan = make_plan(p);
+    const BwdSpace b = carve_bwd(p, plan);
+    Pass<Tin> f{};  // in the direction of time: dq = A(do, v, k), state S^T
+    f.geom = p.geom;
+    f.g = g;
+    f.g_per_head = g_per_head;
+    f.mask = mask;
+    f.seg = plan.seg;
+    Pass<Tin> r = f;  // against it
+    r.pair_scale = r.key_scale = scale;
+    r.inter_scale = 1.f;
+    f.pair_scale = f.inter_scale = scale;
+    f.key_scale = 1.f;
+    f.init = s0;
+    r.init = dsT;
+    if (plan.split) {
+        Pass<Tin> a = f;
+        a.y = k;
+        a.z = v;
+        cudaError_t e = run_segments<Tin, false>(a, p, s0, ws, b.fwd, stream);
+        if (e != cudaSuccess) return e;
+        a = r;
+        a.y = q;
+        a.z = dout;
+        e = run_segments<Tin, true>(a, p, dsT, ws, b.rev, stream);
+        if (e != cudaSuccess) return e;
+        f.init = reinterpret_cast<float*>(ws + b.fwd.state);
+        r.init = reinterpret_cast<float*>(ws + b.rev.state);
+        f.init_by_slot = r.init_by_slot = 1;
+    }
+    f.x = dout;
+    f.y = v;
+    f.z = k;
+    f.out = dq;
+    f.init_transposed = 1;
+    f.dots_stride = r.dots_stride = p.rows();
+    if (dg) {
+        f.dot_with = q;
+        f.dots = reinterpret_cast<float*>(ws + b.qdq);
+        f.ck = ws + b.ck;
+    }
+    cudaError_t e = run_pass<Tin, false, false>(f, p, stream);
+    if (e != cudaSuccess) return e;
+    Pass<Tin> a = r;  // dv = A'(k, q, do), state G
+    a.x = k;
+    a.y = q;
+    a.z = dout;
+    a.out = dv;
+    a.fin = ds0;
+    if (e = run_pass<Tin, true, false>(a, p, stream); e != cudaSuccess) return e;
+    a = r;  // dk = A'(v, do, q), state G^T
+    a.x = v;
+    a.y = dout;
+    a.z = q;
+    a.out = dk;
+    a.init_transposed = 1;
+    if (dg) {
+        a.dot_with = k;
+        a.dots = reinterpret_cast<float*>(ws + b.kdk);
+        a.ck = ws + b.ck;
+        a.ck_dot = reinterpret_cast<float*>(ws + b.ends);
+    }
+    if (e = run_pass<Tin, true, false>(a, p, stream); e != cudaSuccess) return e;
+    if (!dg) return cudaSuccess;
+    const long long slots = p.geom.slots(p.ck_every()), warps = slots * p.geom.H;
+    float* part = reinterpret_cast<float*>(ws + b.part);
+    auto dg_kernel = p.chunked ? la_dg_kernel<Tin, kChunk> : la_dg_kernel<Tin, kRecChunk>;
+    dg_kernel<<<(unsigned)((warps + 3) / 4), 128, 0, stream>>>(
+        p.geom, mask, f.dots, a.dots, p.slabs(), p.rows(), a.ck_dot, g_per_head ? nullptr : dg,
+        g_per_head ? part : nullptr);
+    if (e = cudaGetLastError(); e != cudaSuccess || !g_per_head) return e;
+    la_dg_sum_kernel<Tin><<<p.geom.H, 256, 0, stream>>>(p.geom, part, slots, dg);
+    return cudaGetLastError();
+}
+
+}  // namespace la
+}  // namespace wkv7

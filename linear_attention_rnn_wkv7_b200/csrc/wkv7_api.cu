@@ -13,6 +13,9 @@
 #include "backward.cuh"
 #include "chunked_bwd.cuh"
 #include "gdn_backward.cuh"
+#include "la_passes.cuh"
+#include "la_step.cuh"
+#include "layer_norm.cuh"
 
 namespace {
 
@@ -490,3 +493,5 @@ wkv7_status wkv7_get_last_error(void* stream_) {
 }
 
 }  // extern "C"
+
+#include "la_api.inl"

@@ -85,6 +85,25 @@ def library() -> ctypes.CDLL:
         lib.wkv7_sane_fwd.argtypes = [p] * 9 + [i, p, p, i, i, i, i, i, i, i, p]
         lib.wkv7_sane_step.restype = i
         lib.wkv7_sane_step.argtypes = [p] * 8 + [i, p, p, i, i, i, i, i, p]
+        sz, ll, f = ctypes.c_size_t, ctypes.c_int64, ctypes.c_float
+        lib.wkv7_la_fwd_workspace_bytes.restype = sz
+        lib.wkv7_la_fwd_workspace_bytes.argtypes = [i] * 9
+        lib.wkv7_la_fwd.restype = i
+        lib.wkv7_la_fwd.argtypes = ([p] * 4 + [i] + [p] * 4 + [i] * 5 + [p, i, f, i, i, i, p, sz,
+                                                                        p])
+        lib.wkv7_la_bwd_workspace_bytes.restype = sz
+        lib.wkv7_la_bwd_workspace_bytes.argtypes = [i] * 9
+        lib.wkv7_la_bwd.restype = i
+        lib.wkv7_la_bwd.argtypes = ([p] * 4 + [i] + [p] * 9 + [i] * 5 + [p, i, f, i, i, i, p, sz,
+                                                                        p])
+        lib.wkv7_la_step.restype = i
+        lib.wkv7_la_step.argtypes = [p] * 4 + [i] + [p] * 3 + [i, i, i, i, f, i, p]
+        lib.wkv7_ln_fwd.restype = i
+        lib.wkv7_ln_fwd.argtypes = [p] * 6 + [ll, i, ll, i, f, i, i, p]
+        lib.wkv7_ln_bwd_workspace_bytes.restype = sz
+        lib.wkv7_ln_bwd_workspace_bytes.argtypes = [ll, i, ll, i, i]
+        lib.wkv7_ln_bwd.restype = i
+        lib.wkv7_ln_bwd.argtypes = [p] * 8 + [ll, i, ll, i, i, i, p, sz, p]
         _lib = lib
     return _lib
 
@@ -396,6 +415,18 @@ def wkv7_bwd_noalloc(r, w, k, v, a, b, dout, s0=None, mask=None, dsT=None, cu_se
     return g
 
 
+def _head_norm(o, norm, head_first):
+    """The per-head norm of a mixing op's output; norm = (weight, bias, eps) or None."""
+    if norm is None:
+        return o
+    from .layer_norm import layer_norm
+    weight, bias, eps = norm
+    for name, t in (("weight", weight), ("bias", bias)):
+        if t is not None and t.dim() != 2:
+            raise ValueError(f"norm's {name} must be [H, V], got {tuple(t.shape)}")
+    return layer_norm(o, weight, bias, eps=eps, head_first=head_first)
+
+
 class GeneralizedDeltaRule(torch.autograd.Function):
     """generalized_delta_rule as a differentiable op: forward through wkv7_fwd, backward
     through wkv7_bwd (token-major inputs, K = V = 64, no varlen)."""
@@ -420,12 +451,13 @@ class GeneralizedDeltaRule(torch.autograd.Function):
 
 
 def generalized_delta_rule(r, w, k, v, a, b, initial_state=None, output_final_state=True,
-                           mask=None, cu_seqlens=None, head_first: bool = False):
+                           mask=None, cu_seqlens=None, head_first: bool = False, norm=None):
     """Differentiable forward (README: generalized_delta_rule); returns (o, final state or
-    None).  Backward through wkv7_bwd."""
+    None).  Backward through wkv7_bwd.  norm = (weight, bias, eps): o goes through the norm
+    of each head (layer_norm with weight and bias [H, V], or None)."""
     o, sT = GeneralizedDeltaRule.apply(r, w, k, v, a, b, initial_state, mask, cu_seqlens,
                                        head_first)
-    return o, (sT if output_final_state else None)
+    return _head_norm(o, norm, head_first), (sT if output_final_state else None)
 
 
 def wkv7_gdn_fwd(q, k, v, g, beta, s0=None, cu_seqlens=None, output_final_state: bool = True,
@@ -584,8 +616,8 @@ class GatedDeltaNet(torch.autograd.Function):
 
 
 def gated_delta_net(q, k, v, g, beta, initial_state=None, output_final_state=True,
-                    cu_seqlens=None, head_first: bool = False):
+                    cu_seqlens=None, head_first: bool = False, norm=None):
     """Differentiable Gated DeltaNet (README: gated_delta_net_recurrent / _chunk);
-    returns (o, final state or None)."""
+    returns (o, final state or None).  norm as for generalized_delta_rule."""
     o, sT = GatedDeltaNet.apply(q, k, v, g, beta, initial_state, cu_seqlens, head_first)
-    return o, (sT if output_final_state else None)
+    return _head_norm(o, norm, head_first), (sT if output_final_state else None)
