@@ -6,7 +6,8 @@ namespace {
 bool la_sizes_ok(int B, int T, int H, int K, int V, int N) {
     return B >= 0 && T >= 0 && H > 0 && K > 0 && V > 0 && N >= 0;
 }
-bool la_chunked_ok(int K, wkv7_dtype dtype) { return false; }
+// Whether the tensor-core form exists.
+bool la_chunked_ok(int K, wkv7_dtype dtype) { return dtype == WKV7_BF16 && K <= 128; }
 
 // The problem behind the arguments, or a status.
 wkv7_status la_problem(wkv7::la::Problem& p, int B, int T, int H, int K, int V, int packed,

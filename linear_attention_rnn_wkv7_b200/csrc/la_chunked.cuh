@@ -1,0 +1,875 @@
+// la_chunked.cuh -- one pass of the decay linear attention on tcgen05 tensor cores, in
+// chunks of 128 tokens: bf16, head sizes 64 and 128, forward and backward in time.
+//
+// With c_t the prefix sums of the log decays inside the chunk, U0 the state before the chunk
+// (in the pass's direction), E_ts = e^{c_t - c_s} for s <= t (backward in time: e^{c_s - c_t}
+// for s >= t), f_t = e^{c_t} (e^{c_L - c_t}) and k_s = e^{c_L - c_s} (e^{c_s}):
+//     out = f . (X U0) + (E . X Y^T) Z,        U1 = e^{c_L} U0 + (k . Y)^T Z
+// Four products per chunk:
+//     P  = X Y^T   (128 x 128, contraction D)      then E, the mask and the scale -> bf16
+//     Oi = P Z     (128 x D, contraction 128)      P read from tensor memory
+//     Ox = X U0    (128 x D, contraction D)        U0 rounded to bf16
+//     dU = (k . Y)^T Z   (D x D, contraction 128, twice: k . Y in two bf16 parts)
+// Every exponent is a difference over a stretch of tokens, so decays of any strength are
+// exact (nothing is divided by a small prefix).  X, Y, Z enter raw, as TMA left them.
+//
+// Roundings to bf16: P (as the scores of any attention) and the copy of U0 that Ox reads, each a half
+// step of bf16 of one of the two parts of out.  The state itself is fp32 in registers, and its
+// update's operand is split in two bf16 parts (16 bits), so states and their gradients are as
+// good as fp32's: one bf16 part left the final state 2e-3 off, and two cost one more product
+// on a tensor pipe that is half idle.
+//
+// Bound: 4 tiles of 128 x D bf16 per chunk and SM from and to HBM (1500 ns at D = 64,
+// 3000 ns at D = 128 for a GPU's even share) against about 1200 and 2600 cycles of MMA,
+// so the kernel is built to keep loads in flight.  One persistent CTA of 16 warps per SM, each with
+// one job, so that a chunk's dependent steps overlap with other chunks':
+//     warp 0       TMA loads of X, Y, Z into a ring of stages (4 at D = 64, 2 at D = 128)
+//     warp 1       issues all MMAs
+//     warp 2       decays: prefix sums (64-bit), factors; clears Z's unused rows
+//     warp 3       output tiles shared -> HBM, frees the stage
+//     warps 4-7    P: scores -> E . scores in bf16, in place in tensor memory
+//     warps 8-11   k . Y in two parts over Y (and over X, or a tile of its own);
+//                  the state (all of it at D = 64, half the columns at 128)
+//     warps 12-15  out = f . Ox + Oi; the other half of the state at D = 128
+// The chain from one chunk to the next is only U0 -> bf16 -> (Ox, dU) -> U1; the state never
+// goes through tensor memory.  All waits are on mbarriers and bounded (a second); a thread that
+// gives up sets a flag that ends every other wait, so the CTA always reaches its end, waits
+// for its copies and MMAs in flight (bounded), frees its tensor memory and reports
+// WKV7_ERR_DEVICE_TIMEOUT.
+#pragma once
+#include <cuda.h>
+
+#include <atomic>
+
+#include "chunked.cuh"
+#include "la_common.cuh"
+#include "sm100.cuh"
+
+namespace wkv7 {
+namespace la {
+namespace tc {
+
+using namespace sm100;
+
+constexpr int kThreads = 512;
+constexpr float kLog2e = 1.4426950408889634f;
+
+template <int D>
+struct Cfg {
+    static constexpr int kStages = D == 64 ? 4 : 2;
+    static constexpr int kSub = 128 * 128;            // 128 rows of 64 bf16
+    static constexpr int kTile = (D / 64) * kSub;     // an X, Y, Z or output tile
+    static constexpr int kStage = 3 * kTile;
+    static constexpr int kStateSub = D * 128;         // D rows of 64 bf16
+    static constexpr int kStateBytes = (D / 64) * kStateSub;
+    // k . Y's second part: over X once its products are done, or (room permitting, which
+    // takes that wait off the chain) in a tile of its own
+    static constexpr bool kLoInX = D == 128;
+    static constexpr int kStateWarps = D == 64 ? 4 : 8;
+    static constexpr int OFF_STATE = kStages * kStage;
+    static constexpr int OFF_LO = OFF_STATE + kStateBytes;
+    static constexpr int OFF_SC = OFF_LO + (kLoInX ? 0 : kTile);
+    static constexpr int kScBytes = 2 * 512 + 48;     // c, k, live bits, dead-output bits, decay
+    static constexpr int OFF_BAR = OFF_SC + kStages * kScBytes;
+    static constexpr int kBytes = OFF_BAR + 256;
+    // tensor memory columns
+    static constexpr int TM_P = 0, TM_OI = 128, TM_OX = 128 + D, TM_DU = 128 + 2 * D;
+};
+
+// One stage's decays.
+struct Scan {
+    float c[128];      // prefix sums of log2 decays
+    float k[128];      // key_scale * k_s; 0 for tokens that do not enter
+    uint32_t live[4];  // tokens that enter as keys
+    uint32_t out[4];   // rows that get an output (others are written as 0)
+    float decay;       // e^{c_L}
+};
+
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&h);
+}
+__device__ __forceinline__ void st_shared16(uint32_t addr, uint32_t a, uint32_t b, uint32_t c,
+                                            uint32_t d) {
+    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c),
+                 "r"(d)
+                 : "memory");
+}
+__device__ __forceinline__ void st_shared4(uint32_t addr, uint32_t a) {
+    asm volatile("st.shared.b32 [%0], %1;" ::"r"(addr), "r"(a) : "memory");
+}
+__device__ __forceinline__ uint4 ld_shared16(uint32_t addr) {
+    uint4 v;
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "r"(addr));
+    return v;
+}
+// 32 lanes x 16 columns of packed bf16 pairs.
+__device__ __forceinline__ void tmem_st_raw16(uint32_t taddr, const uint32_t (&v)[16]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, "
+        "%11, %12, %13, %14, %15, %16};" ::"r"(taddr),
+        "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]),
+        "r"(v[8]), "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
+        : "memory");
+}
+// D (tensor memory) += A (tensor memory, bf16 pairs, 8 columns per 16 of the contraction) B.
+__device__ __forceinline__ void umma_bf16_ts(uint32_t tmem_d, uint32_t tmem_a, uint64_t bdesc,
+                                             uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+        " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(tmem_d),
+        "r"(tmem_a), "l"(bdesc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+
+// The CTA's barriers (8 bytes each, from OFF_BAR).
+enum Bar {
+    kFull = 0,     // [4] a stage's tiles have landed
+    kEmpty = 4,    // [4] a stage may be loaded again
+    kScan = 8,     // [4] a stage's decays are there (and its unused Z rows are clear)
+    kStore = 12,   // [4] a stage's output tile is in shared memory
+    kScore = 16,   // [2] P = X Y^T is done
+    kCross = 18,   // [2] Ox = X U0 is done
+    kPReady = 20,  // P in bf16 is in tensor memory
+    kKReady = 21,  // k . Y is in shared memory
+    kSReady = 22,  // U0 in bf16 is in shared memory (and the last dU has been read)
+    kDelta = 23,   // dU is done, and with it every product of the chunk
+    kOFree = 24,   // Ox and Oi have been read
+    kDrain = 25,   // after an abort: all MMAs are done
+    kBars = 26
+};
+
+struct Ctx {
+    uint32_t sbase, bars;
+    volatile int* abort;
+    __device__ __forceinline__ uint32_t bar(int i) const { return bars + 8 * i; }
+    // A bounded wait; false: give up (every role then leaves its loop).
+    __device__ __forceinline__ bool wait(int i, uint32_t parity) const {
+        const uint32_t b = bar(i);
+        if (mbar_try_wait(b, parity)) return true;
+        const uint64_t t0 = globaltimer_ns();
+        for (uint32_t k = 0; k < (1u << 28); ++k) {
+            if (mbar_try_wait(b, parity)) return true;
+            if ((k & 15u) == 15u) {
+                if (*abort) return false;
+                if (globaltimer_ns() - t0 > 1000000000ull) break;
+            }
+        }
+        *abort = 1;
+        raise_flag(4 /* WKV7_ERR_DEVICE_TIMEOUT */);
+        return false;
+    }
+    // The same for a whole warp: all lanes go on, or none (what follows is warp-wide).
+    __device__ __forceinline__ bool wait_warp(int i, uint32_t parity) const {
+        return __all_sync(0xffffffffu, wait(i, parity));
+    }
+    __device__ __forceinline__ void arrive(int i) const { mbar_arrive(bar(i)); }
+};
+
+// The CTA's chunks in order: segments (item) round robin, a segment's chunks in the direction
+// of the pass.  Every role walks the same list.
+template <bool kRev, bool kStateOnly>
+struct Walk {
+    Item it;
+    int h, tb, te, chunks;  // segment [tb, te) of the sequence
+    long long slot, item, items;
+    __device__ __forceinline__ Walk(const Geom& g, int seg)
+        : item((long long)blockIdx.x - gridDim.x), items(g.slots(seg) * g.H) {}
+    // The next segment that has work; false: none left.
+    __device__ __forceinline__ bool next(const Geom& g, int seg) {
+        for (item += gridDim.x; item < items; item += gridDim.x) {
+            slot = item / g.H;
+            h = (int)(item - slot * g.H);
+            it = locate(g, slot, seg);
+            if (it.n < 0) continue;
+            if (kStateOnly && (kRev ? it.j == 0 : it.j == it.nseg - 1)) continue;
+            tb = it.j * seg;
+            te = it.len - tb < seg ? it.len : tb + seg;
+            chunks = (te - tb + kChunk - 1) / kChunk;
+            return true;
+        }
+        return false;
+    }
+    __device__ __forceinline__ int first_token(int i) const {
+        return tb + kChunk * (kRev ? chunks - 1 - i : i);
+    }
+};
+
+// TMA coordinates (1, 2) of the row of token t.
+struct At {
+    int c1, c2;
+};
+__device__ __forceinline__ At tma_row(const Geom& g, const Item& it, int h, int t) {
+    if (g.head_first) return {it.bos + t, it.bb * g.H + h};
+    return {h, it.bb * g.T + it.bos + t};
+}
+
+template <int D, bool kRev, bool kStateOnly>
+__global__ void __launch_bounds__(kThreads, 1)
+la_chunked_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_y,
+                  const __grid_constant__ CUtensorMap tm_z,
+                  const __grid_constant__ CUtensorMap tm_out,
+                  const __grid_constant__ Pass<__nv_bfloat16> p) {
+    using C = Cfg<D>;
+    constexpr int NS = C::kStages;
+    extern __shared__ __align__(1024) uint8_t smem[];
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const Geom& G = p.geom;
+    if (!seqlens_ok(G, tid, kThreads)) {
+        if (tid == 0 && blockIdx.x == 0) raise_flag(5 /* WKV7_ERR_DEVICE_BAD_SEQLENS */);
+        return;
+    }
+    Ctx cx;
+    cx.sbase = smem_u32(smem);
+    cx.bars = cx.sbase + C::OFF_BAR;
+    cx.abort = reinterpret_cast<volatile int*>(smem + C::OFF_BAR + 8 * kBars);
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::OFF_BAR + 8 * kBars + 4);
+    if (cx.sbase & 1023u) {  // the swizzled tiles need a 1024-byte aligned base
+        if (tid == 0) raise_flag(3 /* WKV7_ERR_CUDA */);
+        return;
+    }
+    if (warp == 0) {
+        tmem_alloc(smem_u32(tmem_slot), 512);
+        tmem_relinquish();
+    }
+    if (tid == 32) {
+        *cx.abort = 0;
+        for (int i = 0; i < kBars; ++i) {
+            const int count = i >= kEmpty && i < kEmpty + 4 ? (kStateOnly ? 32 * C::kStateWarps : 1)
+                              : i >= kStore && i < kStore + 4 ? 128
+                              : i == kPReady || i == kKReady || i == kOFree ? 128
+                              : i == kSReady ? 32 * C::kStateWarps
+                                             : 1;
+            mbar_init(cx.bar(i), count);
+        }
+        fence_mbar_init();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+
+    auto scan_of = [&](int st) {
+        return reinterpret_cast<Scan*>(smem + C::OFF_SC + st * C::kScBytes);
+    };
+    Walk<kRev, kStateOnly> wk(G, p.seg);
+    int n = 0;  // chunks so far: stage n % NS, its (n / NS)-th use
+
+    // ------------------------------------------------------------------ warp 0: loads
+    if (warp == 0) {
+        if (lane == 0) {
+            bool ok = true;
+            while (ok && wk.next(G, p.seg)) {
+                for (int i = 0; ok && i < wk.chunks; ++i, ++n) {
+                    const int st = n % NS;
+                    if (n >= NS && !(ok = cx.wait(kEmpty + st, (n / NS - 1) & 1))) break;
+                    const uint32_t full = cx.bar(kFull + st), at = cx.sbase + st * C::kStage;
+                    mbar_arrive_expect_tx(full, (kStateOnly ? 2 : 3) * C::kTile);
+                    const At a = tma_row(G, wk.it, wk.h, wk.first_token(i));
+#pragma unroll
+                    for (int s = 0; s < D / 64; ++s) {
+                        if (!kStateOnly)
+                            tma_load_3d(at + s * C::kSub, &tm_x, full, 64 * s, a.c1, a.c2);
+                        tma_load_3d(at + C::kTile + s * C::kSub, &tm_y, full, 64 * s, a.c1, a.c2);
+                        tma_load_3d(at + 2 * C::kTile + s * C::kSub, &tm_z, full, 64 * s, a.c1,
+                                    a.c2);
+                    }
+                }
+            }
+            if (!ok) {  // the copies in flight land before the CTA leaves (bounded)
+                for (int m = n < NS ? 0 : n - NS; m < n; ++m)
+                    (void)mbar_wait(cx.bar(kFull + m % NS), (m / NS) & 1);
+            }
+        }
+    }
+    // ------------------------------------------------------------------ warp 1: MMAs
+    else if (warp == 1) {
+        if (lane == 0) {
+            bool ok = true;
+            constexpr uint32_t id_score = idesc_bf16(128, 128, false, false);
+            constexpr uint32_t id_out = idesc_bf16(128, D, false, true);
+            constexpr uint32_t id_delta = idesc_bf16(D, D, true, true);
+            auto score = [&](int m) {  // P = X Y^T of chunk m
+                const int st = m % NS;
+                if (!cx.wait(kFull + st, (m / NS) & 1)) return false;
+                tc_fence_after();
+                const uint32_t x = cx.sbase + st * C::kStage, y = x + C::kTile;
+#pragma unroll
+                for (int kk = 0; kk < D / 16; ++kk) {
+                    const uint32_t o = (kk / 4) * C::kSub + (kk % 4) * 32;
+                    umma_bf16(tmem + C::TM_P, smem_desc(x + o, 16, 1024), smem_desc(y + o, 16, 1024),
+                              id_score, kk > 0);
+                }
+                umma_commit(cx.bar(kScore + (m & 1)));
+                return true;
+            };
+            auto chunk = [&](bool more) {  // the products of chunk n (more: another follows)
+                const int st = n % NS;
+                const uint32_t x = cx.sbase + st * C::kStage, y = x + C::kTile, z = y + C::kTile;
+                const uint32_t state = cx.sbase + C::OFF_STATE;
+                if (!cx.wait(kSReady, n & 1)) return false;
+                if (!kStateOnly) {
+                    if (n > 0 && !cx.wait(kOFree, (n - 1) & 1)) return false;
+                    tc_fence_after();
+#pragma unroll
+                    for (int kk = 0; kk < D / 16; ++kk)
+                        umma_bf16(tmem + C::TM_OX,
+                                  smem_desc(x + (kk / 4) * C::kSub + (kk % 4) * 32, 16, 1024),
+                                  smem_desc(state + 2048 * kk, C::kStateSub, 1024), id_out, kk > 0);
+                    if (C::kLoInX) umma_commit(cx.bar(kCross + (n & 1)));
+                    if (!cx.wait(kPReady, n & 1)) return false;
+                    if (!cx.wait(kScan + st, (n / NS) & 1)) return false;  // Z's rows are clear
+                    tc_fence_after();
+#pragma unroll
+                    for (int kk = 0; kk < 8; ++kk)
+                        umma_bf16_ts(tmem + C::TM_OI, tmem + C::TM_P + 8 * kk,
+                                     smem_desc(z + 2048 * kk, C::kSub, 1024), id_out, kk > 0);
+                    if (more && !score(n + 1)) return false;
+                }
+                if (!cx.wait(kKReady, n & 1)) return false;
+                tc_fence_after();
+                const uint32_t lo = C::kLoInX ? x : cx.sbase + C::OFF_LO;
+#pragma unroll
+                for (int kk = 0; kk < 16; ++kk)
+                    umma_bf16(tmem + C::TM_DU,
+                              smem_desc((kk < 8 ? y : lo) + 2048 * (kk % 8), C::kSub, 1024),
+                              smem_desc(z + 2048 * (kk % 8), C::kSub, 1024), id_delta, kk > 0);
+                umma_commit(cx.bar(kDelta));
+                return true;
+            };
+            // chunks left in this and later segments decide whether another score follows
+            bool have = wk.next(G, p.seg);
+            while (have && wk.chunks == 0) have = wk.next(G, p.seg);
+            if (have && !kStateOnly) ok = score(0);
+            while (ok && have) {
+                const int here = wk.chunks;
+                have = wk.next(G, p.seg);
+                while (have && wk.chunks == 0) have = wk.next(G, p.seg);
+                for (int i = 0; ok && i < here; ++i, ++n) ok = chunk(i + 1 < here || have);
+            }
+            if (!ok) {
+                umma_commit(cx.bar(kDrain));
+                (void)mbar_wait(cx.bar(kDrain), 0);
+            }
+        }
+    }
+    // ------------------------------------------------------------------ warp 2: decays
+    else if (warp == 2) {
+        bool ok = true;
+        while (ok && wk.next(G, p.seg)) {
+            const Rows rw = rows_of(G, wk.it, wk.h);
+            const uint8_t* mrow = p.mask ? p.mask + (long long)wk.it.bb * G.T + wk.it.bos : nullptr;
+            const float ghead = p.g_per_head ? to_f32(p.g[wk.h]) : 0.f;
+            for (int i = 0; ok && i < wk.chunks; ++i, ++n) {
+                const int st = n % NS, t0 = wk.first_token(i) + 4 * lane;
+                // four tokens a lane: log2 decays, which tokens enter, which rows get outputs
+                float gl[4];
+                uint32_t in = 0, upd = 0;
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    const int t = t0 + q;
+                    gl[q] = 0.f;
+                    if (t < wk.te) {
+                        in |= 1u << q;
+                        if (!mrow || mrow[t]) {
+                            upd |= 1u << q;
+                            gl[q] = clamp_log_decay(p.g_per_head
+                                                        ? ghead
+                                                        : to_f32(p.g[rw.first + t * rw.step]));
+                        }
+                    }
+                }
+                double c[4];
+                c[0] = gl[0];
+                c[1] = c[0] + gl[1];
+                c[2] = c[1] + gl[2];
+                c[3] = c[2] + gl[3];
+                double inc = c[3];
+#pragma unroll
+                for (int m = 1; m < 32; m <<= 1) {
+                    const double o = __shfl_up_sync(0xffffffffu, inc, m);
+                    if (lane >= m) inc += o;
+                }
+                const double pre = inc - c[3];
+                const double tot = __shfl_sync(0xffffffffu, inc, 31);
+                if (n >= NS && !(ok = cx.wait_warp(kEmpty + st, (n / NS - 1) & 1))) break;
+                Scan* sc = scan_of(st);
+                const uint32_t enter = kRev ? in : upd;
+                float cc[4], kf[4];
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    const double x = pre + c[q];
+                    cc[q] = (float)(x * 1.4426950408889634);
+                    kf[q] = (enter >> q) & 1 ? p.key_scale * expf((float)(kRev ? x : tot - x)) : 0.f;
+                }
+                *reinterpret_cast<float4*>(&sc->c[4 * lane]) = make_float4(cc[0], cc[1], cc[2], cc[3]);
+                *reinterpret_cast<float4*>(&sc->k[4 * lane]) = make_float4(kf[0], kf[1], kf[2], kf[3]);
+                // 8 lanes make a 32-token word
+                uint32_t lw = enter << (4 * (lane & 7)), ow = (kRev ? upd : in) << (4 * (lane & 7));
+#pragma unroll
+                for (int m = 1; m < 8; m <<= 1) {
+                    lw |= __shfl_xor_sync(0xffffffffu, lw, m);
+                    ow |= __shfl_xor_sync(0xffffffffu, ow, m);
+                }
+                if ((lane & 7) == 0) {
+                    sc->live[lane >> 3] = lw;
+                    sc->out[lane >> 3] = ow;
+                }
+                if (lane == 0) sc->decay = (float)exp(tot);
+                // rows of Z that do not enter may hold anything (0 * NaN is NaN): clear them
+                if (__any_sync(0xffffffffu, enter != 15u)) {
+                    if (!(ok = cx.wait_warp(kFull + st, (n / NS) & 1))) break;
+                    const uint32_t z = cx.sbase + st * C::kStage + 2 * C::kTile;
+                    for (int q = 0; q < 4; ++q) {
+                        if ((enter >> q) & 1) continue;
+                        for (int e = 0; e < (D / 64) * 8; ++e)
+                            st_shared16(z + (e >> 3) * C::kSub + (4 * lane + q) * 128 + (e & 7) * 16, 0,
+                                        0, 0, 0);
+                    }
+                    fence_proxy_async();
+                }
+                __syncwarp();
+                if (lane == 0) cx.arrive(kScan + st);
+            }
+        }
+    }
+    // ------------------------------------------------------------------ warp 3: stores
+    else if (warp == 3) {
+        if (!kStateOnly && lane == 0) {
+            bool ok = true;
+            while (ok && wk.next(G, p.seg)) {
+                for (int i = 0; ok && i < wk.chunks; ++i, ++n) {
+                    const int st = n % NS, t0 = wk.first_token(i);
+                    if (!(ok = cx.wait(kStore + st, (n / NS) & 1))) break;
+                    if (t0 + kChunk <= wk.te) {
+                        const uint32_t at = cx.sbase + st * C::kStage + 2 * C::kTile;
+                        const At a = tma_row(G, wk.it, wk.h, t0);
+#pragma unroll
+                        for (int s = 0; s < D / 64; ++s)
+                            tma_store_3d(&tm_out, at + s * C::kSub, 64 * s, a.c1, a.c2);
+                        bulk_commit();
+                        bulk_wait_read0();
+                    }
+                    cx.arrive(kEmpty + st);
+                }
+            }
+            bulk_wait0();
+        }
+    }
+    // ------------------------------------------------------------------ warps 4-7: P
+    else if (warp < 8) {
+        bool ok = true;
+        const int w = warp & 3, row = 32 * w + lane;
+        const uint32_t tp = tmem + ((uint32_t)(32 * w) << 16) + C::TM_P;
+        while (!kStateOnly && ok && wk.next(G, p.seg)) {
+            for (int i = 0; ok && i < wk.chunks; ++i, ++n) {
+                const int st = n % NS;
+                if (!(ok = cx.wait_warp(kScan + st, (n / NS) & 1))) break;
+                const Scan* sc = scan_of(st);
+                const float ct = sc->c[row];
+                if (!(ok = cx.wait_warp(kScore + (n & 1), (n >> 1) & 1))) break;
+                tc_fence_after();
+#pragma unroll
+                for (int b = 0; b < 4; ++b) {
+                    uint32_t out[16];
+                    const bool none = kRev ? b < w : b > w;
+                    if (none) {
+#pragma unroll
+                        for (int q = 0; q < 16; ++q) out[q] = 0;
+                    } else {
+                        const uint32_t live = sc->live[b];
+                        // keys that this row may use: live, and on the diagonal block not
+                        // on the wrong side of the row
+                        uint32_t use = live;
+                        if (b == w) use &= kRev ? 0xffffffffu << lane : 0xffffffffu >> (31 - lane);
+#pragma unroll
+                        for (int half = 0; half < 2; ++half) {
+                            float v[16];
+                            tmem_ld16(tp + 32 * b + 16 * half, v);
+                            tmem_ld_wait();
+#pragma unroll
+                            for (int q = 0; q < 16; q += 4) {
+                                const float4 cs =
+                                    *reinterpret_cast<const float4*>(&sc->c[32 * b + 16 * half + q]);
+                                const float c4[4] = {cs.x, cs.y, cs.z, cs.w};
+#pragma unroll
+                                for (int u = 0; u < 4; ++u) {
+                                    const float e = ex2(kRev ? c4[u] - ct : ct - c4[u]);
+                                    v[q + u] = (use >> (16 * half + q + u)) & 1
+                                                   ? v[q + u] * p.pair_scale * e
+                                                   : 0.f;
+                                }
+                            }
+#pragma unroll
+                            for (int q = 0; q < 8; ++q)
+                                out[8 * half + q] = pack_bf16(v[2 * q], v[2 * q + 1]);
+                        }
+                    }
+                    // in place: block b's 16 columns lie over scores that are read already
+                    tmem_st_raw16(tp + 16 * b, out);
+                }
+                tmem_st_wait();
+                tc_fence_before();
+                cx.arrive(kPReady);
+            }
+        }
+    }
+    // -------------------------------------- warps 8-15: k . Y and state, outputs and state
+    else {
+        bool ok = true;
+        const bool first = warp < 12;      // warps 8-11
+        const int w = warp & 3, wt = tid & 127;
+        constexpr bool kBoth = D == 128;   // warps 12-15 hold state columns 64..127
+        const bool has_state = first || kBoth;
+        constexpr int R = D == 64 ? 32 : 64;  // state entries per thread
+        const int sthread = first ? wt : 128 + wt;
+        constexpr int kSThreads = 32 * C::kStateWarps;
+        // Entry i of a thread: at D = 64 the MMA fragment layout of an M = 64 accumulator (rows
+        // 16 w + lane / 4 and + 8), at D = 128 row 32 w + lane, 64 columns.
+        const int srow = kBoth ? 32 * w + lane : 16 * w + lane / 4;
+        const int scol = kBoth ? (first ? 0 : 64) : 2 * (lane & 3);
+        float S[R];
+        const uint32_t state_s = cx.sbase + C::OFF_STATE;
+        // entries (2 m, 2 m + 1) at D = 64: row srow + 8 (m & 1), columns scol + 8 (m / 2) ..
+        auto load_state = [&](const float* s, bool transposed) {
+            if constexpr (kBoth) {
+                if (!transposed) {
+#pragma unroll
+                    for (int q = 0; q < R; q += 4) {
+                        const float4 x = *reinterpret_cast<const float4*>(s + srow * D + scol + q);
+                        S[q] = x.x; S[q + 1] = x.y; S[q + 2] = x.z; S[q + 3] = x.w;
+                    }
+                } else {
+#pragma unroll
+                    for (int q = 0; q < R; ++q) S[q] = s[(scol + q) * D + srow];
+                }
+            } else {
+#pragma unroll
+                for (int m = 0; m < R / 2; ++m) {
+                    const int r = srow + 8 * (m & 1), c = scol + 8 * (m / 2);
+                    if (!transposed) {
+                        const float2 x = *reinterpret_cast<const float2*>(s + r * D + c);
+                        S[2 * m] = x.x;
+                        S[2 * m + 1] = x.y;
+                    } else {
+                        S[2 * m] = s[c * D + r];
+                        S[2 * m + 1] = s[(c + 1) * D + r];
+                    }
+                }
+            }
+        };
+        auto save_state = [&](float* s, bool transposed) {
+            if constexpr (kBoth) {
+                if (!transposed) {
+#pragma unroll
+                    for (int q = 0; q < R; q += 4)
+                        *reinterpret_cast<float4*>(s + srow * D + scol + q) =
+                            make_float4(S[q], S[q + 1], S[q + 2], S[q + 3]);
+                } else {
+#pragma unroll
+                    for (int q = 0; q < R; ++q) s[(scol + q) * D + srow] = S[q];
+                }
+            } else {
+#pragma unroll
+                for (int m = 0; m < R / 2; ++m) {
+                    const int r = srow + 8 * (m & 1), c = scol + 8 * (m / 2);
+                    if (!transposed) {
+                        *reinterpret_cast<float2*>(s + r * D + c) = make_float2(S[2 * m], S[2 * m + 1]);
+                    } else {
+                        s[c * D + r] = S[2 * m];
+                        s[(c + 1) * D + r] = S[2 * m + 1];
+                    }
+                }
+            }
+        };
+        // U0 in bf16, [row][column] with the columns in 64-wide swizzled blocks
+        auto publish_state = [&]() {
+            if (!kStateOnly) {
+                if constexpr (kBoth) {
+                    const uint32_t base = state_s + (first ? 0 : C::kStateSub) + srow * 128;
+#pragma unroll
+                    for (int q = 0; q < 8; ++q)
+                        st_shared16(base + ((q ^ (srow & 7)) << 4),
+                                    pack_bf16(S[8 * q], S[8 * q + 1]),
+                                    pack_bf16(S[8 * q + 2], S[8 * q + 3]),
+                                    pack_bf16(S[8 * q + 4], S[8 * q + 5]),
+                                    pack_bf16(S[8 * q + 6], S[8 * q + 7]));
+                } else {
+#pragma unroll
+                    for (int m = 0; m < R / 2; ++m) {
+                        const int r = srow + 8 * (m & 1);
+                        st_shared4(state_s + r * 128 + (((m / 2) ^ (r & 7)) << 4) + 4 * (lane & 3),
+                                   pack_bf16(S[2 * m], S[2 * m + 1]));
+                    }
+                }
+                fence_proxy_async();
+            }
+            tc_fence_before();
+            cx.arrive(kSReady);
+        };
+        const bool works = has_state || !kStateOnly;
+        while (ok && works && wk.next(G, p.seg)) {
+            const long long state_at = ((long long)wk.it.n * G.H + wk.h) * D * D;
+            const long long seg_at = (wk.slot * G.H + wk.h) * D * D;
+            const Rows rw = rows_of(G, wk.it, wk.h);
+            if (has_state) {
+                if (!kStateOnly && p.init) {
+                    load_state(p.init + (p.init_by_slot ? seg_at : state_at), p.init_transposed);
+                } else {
+#pragma unroll
+                    for (int q = 0; q < R; ++q) S[q] = 0.f;
+                }
+            }
+            double logs = 0.0;
+            if (has_state && wk.chunks > 0) publish_state();
+            for (int i = 0; ok && i < wk.chunks; ++i, ++n) {
+                const int st = n % NS, t0 = wk.first_token(i);
+                const uint32_t x = cx.sbase + st * C::kStage, y = x + C::kTile, z = y + C::kTile;
+                if (!(ok = cx.wait_warp(kScan + st, (n / NS) & 1))) break;
+                const Scan* sc = scan_of(st);
+                const float decay = sc->decay;
+                if (kStateOnly) logs += (double)sc->c[127];
+                float rowf = 0.f;
+                bool row_out = true;
+                if (!kStateOnly && !first) {
+                    const int row = 32 * w + lane;
+                    rowf = p.inter_scale * ex2(kRev ? sc->c[127] - sc->c[row] : sc->c[row]);
+                    row_out = (sc->out[w] >> lane) & 1;
+                }
+                // Backward in time: <S_end, G_end> of the chunk, with G_end rounded as the
+                // product X U0 reads it.  What tokens s >= t take from it in dL/dc is then
+                // the same sum's own terms, and the difference, e^{c_L - c_t} <S_t, G_end>,
+                // decays with t as it should (with the exact G_end the rounding of all terms
+                // would stay in dg of tokens that G_end no longer reaches).
+                if (kRev && !kStateOnly && p.ck_dot && has_state) {
+                    const long long u = slot_of(G, wk.it, t0 / kChunk, kChunk) * G.H + wk.h;
+                    const float4* ck = static_cast<const float4*>(p.ck) + u * (D * D / 4) + sthread;
+                    float s = 0.f;
+#pragma unroll
+                    for (int q = 0; q < R / 4; ++q) {
+                        const float4 v = ck[q * kSThreads];
+                        const uint32_t a = pack_bf16(S[4 * q], S[4 * q + 1]);
+                        const uint32_t b = pack_bf16(S[4 * q + 2], S[4 * q + 3]);
+                        s = fmaf(v.x, __uint_as_float(a << 16), s);
+                        s = fmaf(v.y, __uint_as_float(a & 0xffff0000u), s);
+                        s = fmaf(v.z, __uint_as_float(b << 16), s);
+                        s = fmaf(v.w, __uint_as_float(b & 0xffff0000u), s);
+                    }
+#pragma unroll
+                    for (int m = 16; m > 0; m >>= 1) s += __shfl_xor_sync(0xffffffffu, s, m);
+                    if (lane == 0) p.ck_dot[u * C::kStateWarps + (sthread >> 5)] = s;
+                }
+
+                if (first) {  // k . Y in two parts
+                    if (!(ok = cx.wait_warp(kFull + st, (n / NS) & 1))) break;
+                    if (!kStateOnly && !(ok = cx.wait_warp(kScore + (n & 1), (n >> 1) & 1))) break;
+                    if (!kStateOnly && C::kLoInX && !(ok = cx.wait_warp(kCross + (n & 1), (n >> 1) & 1)))
+                        break;
+                    const uint32_t lo = C::kLoInX ? x : cx.sbase + C::OFF_LO;
+#pragma unroll 4
+                    for (int u = 0; u < D / 8; ++u) {
+                        const int idx = u * 128 + wt;
+                        const uint32_t at = (idx >> 10) * C::kSub + (idx & 1023) * 16;
+                        const float f = sc->k[(idx & 1023) >> 3];
+                        const uint4 v = ld_shared16(y + at);
+                        const uint32_t in[4] = {v.x, v.y, v.z, v.w};
+                        uint32_t hi[4], lw[4];
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) {
+                            const float a = __uint_as_float(in[q] << 16) * f;
+                            const float b = __uint_as_float(in[q] & 0xffff0000u) * f;
+                            hi[q] = pack_bf16(a, b);
+                            lw[q] = pack_bf16(a - __uint_as_float(hi[q] << 16),
+                                              b - __uint_as_float(hi[q] & 0xffff0000u));
+                            if (f == 0.f) hi[q] = lw[q] = 0;  // whatever the row holds
+                        }
+                        st_shared16(y + at, hi[0], hi[1], hi[2], hi[3]);
+                        st_shared16(lo + at, lw[0], lw[1], lw[2], lw[3]);
+                    }
+                    fence_proxy_async();
+                    cx.arrive(kKReady);
+                }
+
+                if (!(ok = cx.wait_warp(kDelta, n & 1))) break;
+                tc_fence_after();
+                if (has_state) {
+                    if constexpr (kBoth) {
+#pragma unroll
+                        for (int q = 0; q < R; q += 16) {
+                            float d[16];
+                            tmem_ld16(tmem + ((uint32_t)(32 * w) << 16) + C::TM_DU + scol + q, d);
+                            tmem_ld_wait();
+#pragma unroll
+                            for (int u = 0; u < 16; ++u) S[q + u] = fmaf(decay, S[q + u], d[u]);
+                        }
+                    } else {
+#pragma unroll
+                        for (int q = 0; q < R; q += 16) {
+                            float d[16];
+                            tmem_ld16x32(tmem + ((uint32_t)(32 * w) << 16) + C::TM_DU + 2 * q, d);
+                            tmem_ld_wait();
+#pragma unroll
+                            for (int u = 0; u < 16; ++u) S[q + u] = fmaf(decay, S[q + u], d[u]);
+                        }
+                    }
+                    // forward: keep the state at the chunk's end
+                    if (!kRev && !kStateOnly && p.ck) {
+                        const long long u = slot_of(G, wk.it, t0 / kChunk, kChunk) * G.H + wk.h;
+                        float4* ck = static_cast<float4*>(p.ck) + u * (D * D / 4) + sthread;
+#pragma unroll
+                        for (int q = 0; q < R / 4; ++q)
+                            ck[q * kSThreads] =
+                                make_float4(S[4 * q], S[4 * q + 1], S[4 * q + 2], S[4 * q + 3]);
+                    }
+                    // the next chunk's U0 (every product that reads the last one is done)
+                    if (i + 1 < wk.chunks) publish_state();
+                    if (kStateOnly) cx.arrive(kEmpty + st);
+                }
+
+                if (!kStateOnly && !first) {  // outputs
+                    const int row = 32 * w + lane, t = t0 + row;
+                    const bool in = t < wk.te, whole = t0 + kChunk <= wk.te;
+                    const long long grow = rw.first + (long long)t * rw.step;
+                    const uint32_t to = tmem + ((uint32_t)(32 * w) << 16);
+                    float dot = 0.f;
+#pragma unroll
+                    for (int q = 0; q < D; q += 16) {
+                        float ox[16], oi[16];
+                        tmem_ld16(to + C::TM_OX + q, ox);
+                        tmem_ld16(to + C::TM_OI + q, oi);
+                        uint4 wv[2];
+                        if (p.dots && in && row_out) {
+                            const uint4* src =
+                                reinterpret_cast<const uint4*>(p.dot_with + grow * D + q);
+                            wv[0] = src[0];
+                            wv[1] = src[1];
+                        }
+                        tmem_ld_wait();
+                        uint32_t pk[8];
+#pragma unroll
+                        for (int u = 0; u < 16; ++u) ox[u] = fmaf(rowf, ox[u], oi[u]);
+                        if (!row_out) {
+#pragma unroll
+                            for (int u = 0; u < 16; ++u) ox[u] = 0.f;
+                        }
+                        if (p.dots && in && row_out) {
+                            const uint32_t ww[8] = {wv[0].x, wv[0].y, wv[0].z, wv[0].w,
+                                                    wv[1].x, wv[1].y, wv[1].z, wv[1].w};
+#pragma unroll
+                            for (int u = 0; u < 8; ++u) {
+                                dot = fmaf(ox[2 * u], __uint_as_float(ww[u] << 16), dot);
+                                dot = fmaf(ox[2 * u + 1], __uint_as_float(ww[u] & 0xffff0000u), dot);
+                            }
+                        }
+#pragma unroll
+                        for (int u = 0; u < 8; ++u) pk[u] = pack_bf16(ox[2 * u], ox[2 * u + 1]);
+                        if (whole) {
+                            const uint32_t base = z + (q / 64) * C::kSub + row * 128;
+                            const int c = (q % 64) / 8;
+                            st_shared16(base + ((c ^ (row & 7)) << 4), pk[0], pk[1], pk[2], pk[3]);
+                            st_shared16(base + (((c + 1) ^ (row & 7)) << 4), pk[4], pk[5], pk[6],
+                                        pk[7]);
+                        } else if (in) {
+                            uint4* dst = reinterpret_cast<uint4*>(p.out + grow * D + q);
+                            dst[0] = make_uint4(pk[0], pk[1], pk[2], pk[3]);
+                            dst[1] = make_uint4(pk[4], pk[5], pk[6], pk[7]);
+                        }
+                    }
+                    tc_fence_before();
+                    cx.arrive(kOFree);
+                    if (p.dots && in) p.dots[grow] = dot;
+                    fence_proxy_async();
+                    cx.arrive(kStore + st);
+                }
+            }
+            if (!ok) break;
+            if (has_state) {
+                if (kStateOnly) {
+                    save_state(p.seg_state + seg_at, p.init_transposed);
+                    if (sthread == 0)
+                        p.seg_decay[wk.slot * G.H + wk.h] = (float)exp2(logs);
+                } else if (p.fin && (kRev ? wk.it.j == 0 : wk.it.j == wk.it.nseg - 1)) {
+                    save_state(p.fin + state_at, p.init_transposed);
+                }
+            }
+        }
+    }
+    __syncwarp();
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == 0) tmem_dealloc(tmem, 512);
+}
+
+// [B*T, H, D] bf16 as (D, H, B*T), box 64 x 1 x 128 rows; head first [B*H, T, D] as
+// (D, T, B*H), box 64 x 128 x 1.  Either box lands as 128 swizzled rows of 128 bytes.
+inline bool make_map(CUtensorMap* map, const void* ptr, int B, const Geom& g, int D) {
+    chunked::EncodeTiledFn enc = chunked::encode_fn();
+    if (!enc) return false;
+    cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)g.H, (cuuint64_t)B * g.T};
+    cuuint64_t strides[2] = {(cuuint64_t)D * 2, (cuuint64_t)g.H * D * 2};
+    cuuint32_t box[3] = {64, 1, 128};
+    if (g.head_first) {
+        dims[1] = (cuuint64_t)g.T;
+        dims[2] = (cuuint64_t)B * g.H;
+        strides[1] = (cuuint64_t)g.T * D * 2;
+        box[1] = 128;
+        box[2] = 1;
+    }
+    cuuint32_t estr[3] = {1, 1, 1};
+    return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(ptr), dims, strides, box,
+               estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+               CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// SMs of the current device and the kernel's shared-memory size, set once per device.
+template <int D, bool kRev, bool kStateOnly>
+inline int prepare_device() {
+    constexpr int kMaxDev = 64;
+    static std::atomic<int> sms[kMaxDev];
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDev) return 0;
+    int n = sms[dev].load(std::memory_order_acquire);
+    if (n > 0) return n;
+    if (cudaFuncSetAttribute(la_chunked_kernel<D, kRev, kStateOnly>,
+                             cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             Cfg<D>::kBytes) != cudaSuccess ||
+        cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+        return 0;
+    sms[dev].store(n, std::memory_order_release);
+    return n;
+}
+
+template <int D, bool kRev, bool kStateOnly>
+inline cudaError_t launch_d(const Pass<__nv_bfloat16>& p, int B, cudaStream_t stream) {
+    const int sms = prepare_device<D, kRev, kStateOnly>();
+    if (sms <= 0) {
+        const cudaError_t e = cudaGetLastError();
+        return e != cudaSuccess ? e : cudaErrorInvalidDevice;
+    }
+    CUtensorMap m[4];
+    const void* ptr[4] = {kStateOnly ? p.y : p.x, p.y, p.z, kStateOnly ? p.y : p.out};
+    for (int i = 0; i < 4; ++i)
+        if (!make_map(&m[i], ptr[i], B, p.geom, D)) return cudaErrorInvalidValue;
+    const long long items = p.geom.slots(p.seg) * p.geom.H;
+    const unsigned grid = (unsigned)(items < sms ? items : sms);
+    la_chunked_kernel<D, kRev, kStateOnly><<<grid, kThreads, Cfg<D>::kBytes, stream>>>(m[0], m[1], m[2],
+                                                                                 m[3], p);
+    return cudaGetLastError();
+}
+template <bool kRev, bool kStateOnly>
+inline cudaError_t launch_pass(const Pass<__nv_bfloat16>& p, int B, int D, cudaStream_t stream) {
+    return D == 64 ? launch_d<64, kRev, kStateOnly>(p, B, stream)
+                   : launch_d<128, kRev, kStateOnly>(p, B, stream);
+}
+
+}  // namespace tc
+}  // namespace la
+}  // namespace wkv7

@@ -150,7 +150,7 @@ struct Pass {
     float* dots;          // [slab][rows]
     long long dots_stride;
     void* ck;             // states at each chunk's end (layout private to the kernel)
-    float* ck_dot;        // [chunk slot][H][slab]: <ck, state before the chunk>
+    float* ck_dot;        // [chunk slot][H][parts]: parts of <ck, state before the chunk>
 };
 
 // ---- start states of the segments --------------------------------------------------------
@@ -205,7 +205,8 @@ template <typename Tin, int kC>
 __global__ void __launch_bounds__(128)
 la_dg_kernel(Geom g, const uint8_t* __restrict__ mask, const float* __restrict__ qdq,
              const float* __restrict__ kdk, int slabs, long long stride,
-             const float* __restrict__ ends, Tin* __restrict__ dg, float* __restrict__ part) {
+             const float* __restrict__ ends, int nends, Tin* __restrict__ dg,
+             float* __restrict__ part) {
     if (!seqlens_ok(g, threadIdx.x, 128)) return;
     constexpr int kPer = kC / 32;
     const int lane = threadIdx.x & 31;
@@ -244,7 +245,7 @@ la_dg_kernel(Geom g, const uint8_t* __restrict__ mask, const float* __restrict__
     }
     after = __shfl_down_sync(0xffffffffu, run, 1);
     if (lane == 31) after = 0.f;
-    for (int s = 0; s < slabs; ++s) after += ends[id * slabs + s];
+    for (int s = 0; s < nends; ++s) after += ends[id * nends + s];
     float sum = 0.f;
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {

@@ -4,6 +4,7 @@
 #include <algorithm>
 
 #include "la_common.cuh"
+#include "la_chunked.cuh"
 #include "la_recurrent.cuh"
 
 namespace wkv7 {
@@ -18,6 +19,8 @@ struct Problem {
     int ck_every() const { return chunked ? kChunk : kRecChunk; }
     // column slabs that one (segment, head) is split into
     int slabs() const { return chunked ? 1 : D / 64; }
+    // parts of a chunk's <S_end, G_end>
+    int ends() const { return chunked ? D / 16 : D / 64; }
 };
 
 // Segments.  One segment per sequence needs nothing extra.  With fewer (sequence, head)
@@ -93,7 +96,7 @@ inline BwdSpace carve_bwd(const Problem& p, const Plan& plan) {
     b.qdq = c.take(dots);
     b.kdk = c.take(dots);
     b.ck = c.take(units * p.D * p.D * sizeof(float));
-    b.ends = c.take(units * p.slabs() * sizeof(float));
+    b.ends = c.take(units * p.ends() * sizeof(float));
     b.part = c.take(units * sizeof(float));
     b.bytes = c.at;
     return b;
@@ -107,6 +110,11 @@ inline size_t bwd_workspace(const Problem& p) { return carve_bwd(p, make_plan(p)
 
 template <typename Tin, bool kRev, bool kStateOnly>
 inline cudaError_t run_pass(const Pass<Tin>& a, const Problem& p, cudaStream_t stream) {
+    if constexpr (sizeof(Tin) == 2) {
+        // (without a token there are no tensors to map: only states are copied)
+        if (p.chunked && p.geom.T > 0)
+            return tc::launch_pass<kRev, kStateOnly>(a, p.B, p.D, stream);
+    }
     return launch_recurrent_pass<Tin, kRev, kStateOnly>(a, p.D, stream);
 }
 
@@ -228,7 +236,8 @@ inline cudaError_t backward(const Problem& p, const Tin* q, const Tin* k, const 
     float* part = reinterpret_cast<float*>(ws + b.part);
     auto dg_kernel = p.chunked ? la_dg_kernel<Tin, kChunk> : la_dg_kernel<Tin, kRecChunk>;
     dg_kernel<<<(unsigned)((warps + 3) / 4), 128, 0, stream>>>(
-        p.geom, mask, f.dots, a.dots, p.slabs(), p.rows(), a.ck_dot, g_per_head ? nullptr : dg,
+        p.geom, mask, f.dots, a.dots, p.slabs(), p.rows(), a.ck_dot, p.ends(),
+        g_per_head ? nullptr : dg,
         g_per_head ? part : nullptr);
     if (e = cudaGetLastError(); e != cudaSuccess || !g_per_head) return e;
     la_dg_sum_kernel<Tin><<<p.geom.H, 256, 0, stream>>>(p.geom, part, slots, dg);

@@ -348,9 +348,6 @@ la_recurrent_kernel(const Pass<Tin> p) {
     } else if (p.fin && (kRev ? it.j == 0 : it.j == it.nseg - 1)) {
         store_tile<D>(p.fin + state_at, p.init_transposed, row0, col0, S);
     }
-    // a chunk that no token reaches (an empty sequence) has no <S_end, G_end>
-    if (kRev && !kStateOnly && p.ck_dot && it.len == 0 && tid == 0)
-        p.ck_dot[(slot_of(G, it, 0, kRecChunk) * G.H + h) * C::kSlabs + slab] = 0.f;
 }
 
 template <typename Tin, int D, bool kRev, bool kStateOnly>
