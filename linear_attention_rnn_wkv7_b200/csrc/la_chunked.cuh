@@ -56,34 +56,39 @@ constexpr float kLog2e = 1.4426950408889634f;
 
 template <int D>
 struct Cfg {
-    static constexpr int kStages = D == 64 ? 4 : 2;
+    static constexpr int kStages = D == 64 ? 3 : 2;
     static constexpr int kSub = 128 * 128;            // 128 rows of 64 bf16
     static constexpr int kTile = (D / 64) * kSub;     // an X, Y, Z or output tile
     static constexpr int kStage = 3 * kTile;
     static constexpr int kStateSub = D * 128;         // D rows of 64 bf16
     static constexpr int kStateBytes = (D / 64) * kStateSub;
-    // k . Y's second part: over X once its products are done, or (room permitting, which
-    // takes that wait off the chain) in a tile of its own
-    static constexpr bool kLoInX = D == 128;
+    // The second and third part of k . Y: over X and over U0's copy once their products are
+    // done, or (where there is room) in tiles of their own, which takes that wait off the
+    // chain.
+    static constexpr bool kPartsInPlace = D == 128;
     static constexpr int kStateWarps = D == 64 ? 4 : 8;
     static constexpr int OFF_STATE = kStages * kStage;
-    static constexpr int OFF_LO = OFF_STATE + kStateBytes;
-    static constexpr int OFF_SC = OFF_LO + (kLoInX ? 0 : kTile);
-    static constexpr int kScBytes = 2 * 512 + 48;     // c, k, live bits, dead-output bits, decay
+    static constexpr int OFF_PARTS = OFF_STATE + kStateBytes;
+    static constexpr int OFF_SC = OFF_PARTS + (kPartsInPlace ? 0 : 2 * kTile);
+    static constexpr int kScBytes = 2 * 512 + 64;     // struct Scan
     static constexpr int OFF_BAR = OFF_SC + kStages * kScBytes;
     static constexpr int kBytes = OFF_BAR + 256;
     // tensor memory columns
     static constexpr int TM_P = 0, TM_OI = 128, TM_OX = 128 + D, TM_DU = 128 + 2 * D;
 };
 
-// One stage's decays.
+// One stage's decays.  Tokens come in blocks of 32; a block's border is its last token
+// (backward in time: its first), the nearest to the tokens that its keys reach.
 struct Scan {
     float c[128];      // prefix sums of log2 decays
-    float k[128];      // key_scale * k_s; 0 for tokens that do not enter
+    float f[128];      // from the token to its block's border; 0 for tokens that do not enter
+    float kb[4];       // key_scale * from the block's border to the chunk's end: k_s = f kb
     uint32_t live[4];  // tokens that enter as keys
     uint32_t out[4];   // rows that get an output (others are written as 0)
     float decay;       // e^{c_L}
+    float pad[3];
 };
+static_assert(sizeof(Scan) == 1088, "kScBytes");
 
 __device__ __forceinline__ float ex2(float x) {
     float y;
@@ -110,6 +115,23 @@ __device__ __forceinline__ uint4 ld_shared16(uint32_t addr) {
                  : "r"(addr));
     return v;
 }
+// 32 lanes x 32 columns: thread i gets lane i's.
+__device__ __forceinline__ void tmem_ld32(uint32_t taddr, float (&v)[32]) {
+    uint32_t r[32];
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, "
+        "%11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, "
+        "%28, %29, %30, %31}, [%32];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+          "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]),
+          "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]),
+          "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+          "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]),
+          "=r"(r[31])
+        : "r"(taddr));
+#pragma unroll
+    for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
+}
 // 32 lanes x 16 columns of packed bf16 pairs.
 __device__ __forceinline__ void tmem_st_raw16(uint32_t taddr, const uint32_t (&v)[16]) {
     asm volatile(
@@ -118,6 +140,12 @@ __device__ __forceinline__ void tmem_st_raw16(uint32_t taddr, const uint32_t (&v
         "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]),
         "r"(v[8]), "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
         : "memory");
+}
+// One lane of a converged warp.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile("{\n .reg .pred e;\n elect.sync _|e, 0xffffffff;\n selp.u32 %0, 1, 0, e;\n}\n" : "=r"(p));
+    return p != 0;
 }
 // D (tensor memory) += A (tensor memory, bf16 pairs, 8 columns per 16 of the contraction) B.
 __device__ __forceinline__ void umma_bf16_ts(uint32_t tmem_d, uint32_t tmem_a, uint64_t bdesc,
@@ -146,25 +174,31 @@ enum Bar {
     kBars = 26
 };
 
+// The slow path of a wait, kept out of line (the roles' code has to fit the instruction
+// caches): polls for at most a second, or until another thread has given up.
+__device__ __noinline__ bool wait_slow(uint32_t bar, uint32_t parity, volatile int* abort) {
+    uint64_t t0 = 0;
+    for (uint32_t k = 0; k < (1u << 28); ++k) {
+        if (mbar_try_wait(bar, parity)) return true;
+        if ((k & 63u) == 63u) {  // (the timer is slow to read: not before it matters)
+            if (*abort) return false;
+            const uint64_t now = globaltimer_ns();
+            if (t0 == 0) t0 = now;
+            if (now - t0 > 1000000000ull) break;
+        }
+    }
+    *abort = 1;
+    raise_flag(4 /* WKV7_ERR_DEVICE_TIMEOUT */);
+    return false;
+}
+
 struct Ctx {
     uint32_t sbase, bars;
     volatile int* abort;
     __device__ __forceinline__ uint32_t bar(int i) const { return bars + 8 * i; }
     // A bounded wait; false: give up (every role then leaves its loop).
     __device__ __forceinline__ bool wait(int i, uint32_t parity) const {
-        const uint32_t b = bar(i);
-        if (mbar_try_wait(b, parity)) return true;
-        const uint64_t t0 = globaltimer_ns();
-        for (uint32_t k = 0; k < (1u << 28); ++k) {
-            if (mbar_try_wait(b, parity)) return true;
-            if ((k & 15u) == 15u) {
-                if (*abort) return false;
-                if (globaltimer_ns() - t0 > 1000000000ull) break;
-            }
-        }
-        *abort = 1;
-        raise_flag(4 /* WKV7_ERR_DEVICE_TIMEOUT */);
-        return false;
+        return mbar_try_wait(bar(i), parity) || wait_slow(bar(i), parity, abort);
     }
     // The same for a whole warp: all lanes go on, or none (what follows is warp-wide).
     __device__ __forceinline__ bool wait_warp(int i, uint32_t parity) const {
@@ -173,32 +207,67 @@ struct Ctx {
     __device__ __forceinline__ void arrive(int i) const { mbar_arrive(bar(i)); }
 };
 
+// A role's place in the list of chunks: the n-th of the CTA, in stage st for the ph-th time.
+template <int NS>
+struct Place {
+    int n = 0, st = 0;
+    uint32_t ph = 0;
+    __device__ __forceinline__ void next() {
+        ++n;
+        if (++st == NS) {
+            st = 0;
+            ph ^= 1;
+        }
+    }
+    __device__ __forceinline__ uint32_t odd() const { return n & 1; }          // one barrier
+    __device__ __forceinline__ uint32_t pair() const { return (n >> 1) & 1; }  // two in turn
+};
+
 // The CTA's chunks in order: segments (item) round robin, a segment's chunks in the direction
-// of the pass.  Every role walks the same list.
-template <bool kRev, bool kStateOnly>
-struct Walk {
+// of the pass.  Every role walks the same list.  (Slot and item numbers fit 32 bits: the
+// entry points check.)
+struct Seg {
     Item it;
-    int h, tb, te, chunks;  // segment [tb, te) of the sequence
-    long long slot, item, items;
+    int h, slot, tb, te, chunks;  // segment [tb, te) of the sequence
+};
+// The item if it has work (chunks >= 0).  Out of line: divisions, in every role.
+__device__ __noinline__ Seg find_item(const Geom& g, int seg, int item, int rev, int state_only) {
+    Seg s;
+    s.slot = item / g.H;
+    s.h = item - s.slot * g.H;
+    s.it = locate(g, s.slot, seg);
+    s.tb = s.te = 0;
+    s.chunks = -1;
+    if (s.it.n < 0) return s;
+    if (state_only && (rev ? s.it.j == 0 : s.it.j == s.it.nseg - 1)) return s;
+    s.tb = s.it.j * seg;
+    s.te = s.it.len - s.tb < seg ? s.it.len : s.tb + seg;
+    s.chunks = (s.te - s.tb + kChunk - 1) / kChunk;
+    return s;
+}
+template <bool kRev, bool kStateOnly>
+struct Walk : Seg {
+    int item, items;
     __device__ __forceinline__ Walk(const Geom& g, int seg)
-        : item((long long)blockIdx.x - gridDim.x), items(g.slots(seg) * g.H) {}
+        : item((int)blockIdx.x - (int)gridDim.x), items((int)(g.slots(seg) * g.H)) {}
     // The next segment that has work; false: none left.
     __device__ __forceinline__ bool next(const Geom& g, int seg) {
-        for (item += gridDim.x; item < items; item += gridDim.x) {
-            slot = item / g.H;
-            h = (int)(item - slot * g.H);
-            it = locate(g, slot, seg);
-            if (it.n < 0) continue;
-            if (kStateOnly && (kRev ? it.j == 0 : it.j == it.nseg - 1)) continue;
-            tb = it.j * seg;
-            te = it.len - tb < seg ? it.len : tb + seg;
-            chunks = (te - tb + kChunk - 1) / kChunk;
-            return true;
+        while (items - item > (int)gridDim.x) {
+            item += gridDim.x;
+            static_cast<Seg&>(*this) = find_item(g, seg, item, kRev, kStateOnly);
+            if (this->chunks >= 0) return true;
         }
         return false;
     }
     __device__ __forceinline__ int first_token(int i) const {
-        return tb + kChunk * (kRev ? chunks - 1 - i : i);
+        return this->tb + kChunk * (kRev ? this->chunks - 1 - i : i);
+    }
+    // Number of the chunk that starts at token t0 (128-token slots of all sequences) and head.
+    __device__ __forceinline__ long long unit(const Geom& g, int t0) const {
+        const int c = t0 / kChunk;
+        const int slot = g.cu ? this->it.bos / kChunk + this->it.n + c
+                              : this->it.n * Geom::segs(g.T, kChunk) + c;
+        return (long long)slot * g.H + this->h;
     }
 };
 
@@ -260,16 +329,17 @@ la_chunked_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constan
         return reinterpret_cast<Scan*>(smem + C::OFF_SC + st * C::kScBytes);
     };
     Walk<kRev, kStateOnly> wk(G, p.seg);
-    int n = 0;  // chunks so far: stage n % NS, its (n / NS)-th use
+    Place<NS> at_;
+    int& n = at_.n;
 
     // ------------------------------------------------------------------ warp 0: loads
     if (warp == 0) {
         if (lane == 0) {
             bool ok = true;
             while (ok && wk.next(G, p.seg)) {
-                for (int i = 0; ok && i < wk.chunks; ++i, ++n) {
-                    const int st = n % NS;
-                    if (n >= NS && !(ok = cx.wait(kEmpty + st, (n / NS - 1) & 1))) break;
+                for (int i = 0; ok && i < wk.chunks; ++i, at_.next()) {
+                    const int st = at_.st;
+                    if (n >= NS && !(ok = cx.wait(kEmpty + st, at_.ph ^ 1))) break;
                     const uint32_t full = cx.bar(kFull + st), at = cx.sbase + st * C::kStage;
                     mbar_arrive_expect_tx(full, (kStateOnly ? 2 : 3) * C::kTile);
                     const At a = tma_row(G, wk.it, wk.h, wk.first_token(i));
@@ -291,71 +361,95 @@ la_chunked_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constan
     }
     // ------------------------------------------------------------------ warp 1: MMAs
     else if (warp == 1) {
-        if (lane == 0) {
+        {
+            // The whole warp walks the list, so that descriptors stay in uniform registers (an
+            // MMA takes its operands from there); one elected lane issues.
+            const bool leader = elect_one();
+            const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_slot, 0);
             bool ok = true;
             constexpr uint32_t id_score = idesc_bf16(128, 128, false, false);
             constexpr uint32_t id_out = idesc_bf16(128, D, false, true);
             constexpr uint32_t id_delta = idesc_bf16(D, D, true, true);
-            auto score = [&](int m) {  // P = X Y^T of chunk m
-                const int st = m % NS;
-                if (!cx.wait(kFull + st, (m / NS) & 1)) return false;
+            // descriptors: an address in 16-byte units added to the layout's constants
+            const uint64_t kmaj = smem_desc(0, 16, 1024);                  // K-major
+            const uint64_t mn_tile = smem_desc(0, C::kSub, 1024);          // MN-major tiles
+            const uint64_t mn_state = smem_desc(0, C::kStateSub, 1024);    // MN-major U0
+            Place<NS> sc_at;
+            auto score = [&]() {  // P = X Y^T of the next chunk
+                const int st = sc_at.st, m = sc_at.n;
+                if (!cx.wait_warp(kFull + st, sc_at.ph)) return false;
+                sc_at.next();
                 tc_fence_after();
-                const uint32_t x = cx.sbase + st * C::kStage, y = x + C::kTile;
+                uint64_t a = kmaj + ((cx.sbase + st * C::kStage) >> 4), b = a + (C::kTile >> 4);
+#pragma unroll 1
+                for (int s = 0; s < D / 64; ++s) {
 #pragma unroll
-                for (int kk = 0; kk < D / 16; ++kk) {
-                    const uint32_t o = (kk / 4) * C::kSub + (kk % 4) * 32;
-                    umma_bf16(tmem + C::TM_P, smem_desc(x + o, 16, 1024), smem_desc(y + o, 16, 1024),
-                              id_score, kk > 0);
+                    for (int kk = 0; kk < 4; ++kk)
+                        if (leader) umma_bf16(tmem + C::TM_P, a + 2 * kk, b + 2 * kk, id_score, s + kk > 0);
+                    a += C::kSub >> 4;
+                    b += C::kSub >> 4;
                 }
-                umma_commit(cx.bar(kScore + (m & 1)));
+                if (leader) umma_commit(cx.bar(kScore + (m & 1)));
                 return true;
             };
             auto chunk = [&](bool more) {  // the products of chunk n (more: another follows)
-                const int st = n % NS;
-                const uint32_t x = cx.sbase + st * C::kStage, y = x + C::kTile, z = y + C::kTile;
-                const uint32_t state = cx.sbase + C::OFF_STATE;
-                if (!cx.wait(kSReady, n & 1)) return false;
+                const int st = at_.st;
+                const uint32_t x = (cx.sbase + st * C::kStage) >> 4, y = x + (C::kTile >> 4),
+                               z = y + (C::kTile >> 4), state = (cx.sbase + C::OFF_STATE) >> 4;
+                if (!cx.wait_warp(kSReady, at_.odd())) return false;
                 if (!kStateOnly) {
-                    if (n > 0 && !cx.wait(kOFree, (n - 1) & 1)) return false;
+                    if (n > 0 && !cx.wait_warp(kOFree, at_.odd() ^ 1)) return false;
                     tc_fence_after();
+                    uint64_t a = kmaj + x, b = mn_state + state;
+#pragma unroll 1
+                    for (int s = 0; s < D / 64; ++s) {
 #pragma unroll
-                    for (int kk = 0; kk < D / 16; ++kk)
-                        umma_bf16(tmem + C::TM_OX,
-                                  smem_desc(x + (kk / 4) * C::kSub + (kk % 4) * 32, 16, 1024),
-                                  smem_desc(state + 2048 * kk, C::kStateSub, 1024), id_out, kk > 0);
-                    if (C::kLoInX) umma_commit(cx.bar(kCross + (n & 1)));
-                    if (!cx.wait(kPReady, n & 1)) return false;
-                    if (!cx.wait(kScan + st, (n / NS) & 1)) return false;  // Z's rows are clear
+                        for (int kk = 0; kk < 4; ++kk)
+                            if (leader) umma_bf16(tmem + C::TM_OX, a + 2 * kk, b + 128 * kk, id_out, s + kk > 0);
+                        a += C::kSub >> 4;
+                        b += 512;
+                    }
+                    if (C::kPartsInPlace && leader) umma_commit(cx.bar(kCross + (n & 1)));
+                    if (!cx.wait_warp(kPReady, at_.odd())) return false;
+                    if (!cx.wait_warp(kScan + st, at_.ph)) return false;  // Z's rows are clear
                     tc_fence_after();
+                    b = mn_tile + z;
 #pragma unroll
                     for (int kk = 0; kk < 8; ++kk)
-                        umma_bf16_ts(tmem + C::TM_OI, tmem + C::TM_P + 8 * kk,
-                                     smem_desc(z + 2048 * kk, C::kSub, 1024), id_out, kk > 0);
-                    if (more && !score(n + 1)) return false;
+                        if (leader) umma_bf16_ts(tmem + C::TM_OI, tmem + C::TM_P + 8 * kk, b + 128 * kk, id_out,
+                                     kk > 0);
+                    if (more && !score()) return false;
                 }
-                if (!cx.wait(kKReady, n & 1)) return false;
+                if (!cx.wait_warp(kKReady, at_.odd())) return false;
                 tc_fence_after();
-                const uint32_t lo = C::kLoInX ? x : cx.sbase + C::OFF_LO;
+                // the parts of k . Y: over Y, and over X and U0 or in their own tiles
+                const uint32_t own = (cx.sbase + C::OFF_PARTS) >> 4;
+#pragma unroll 1
+                for (int part = 0; part < p.parts; ++part) {
+                    const uint64_t a =
+                        mn_tile + (part == 0             ? y
+                                   : C::kPartsInPlace    ? (part == 1 ? x : state)
+                                                         : own + (part - 1) * (C::kTile >> 4));
 #pragma unroll
-                for (int kk = 0; kk < 16; ++kk)
-                    umma_bf16(tmem + C::TM_DU,
-                              smem_desc((kk < 8 ? y : lo) + 2048 * (kk % 8), C::kSub, 1024),
-                              smem_desc(z + 2048 * (kk % 8), C::kSub, 1024), id_delta, kk > 0);
-                umma_commit(cx.bar(kDelta));
+                    for (int kk = 0; kk < 8; ++kk)
+                        if (leader) umma_bf16(tmem + C::TM_DU, a + 128 * kk, mn_tile + z + 128 * kk, id_delta,
+                                  part + kk > 0);
+                }
+                if (leader) umma_commit(cx.bar(kDelta));
                 return true;
             };
             // chunks left in this and later segments decide whether another score follows
             bool have = wk.next(G, p.seg);
             while (have && wk.chunks == 0) have = wk.next(G, p.seg);
-            if (have && !kStateOnly) ok = score(0);
+            if (have && !kStateOnly) ok = score();
             while (ok && have) {
-                const int here = wk.chunks;
+                const int here = __shfl_sync(0xffffffffu, wk.chunks, 0);
                 have = wk.next(G, p.seg);
                 while (have && wk.chunks == 0) have = wk.next(G, p.seg);
-                for (int i = 0; ok && i < here; ++i, ++n) ok = chunk(i + 1 < here || have);
+                for (int i = 0; ok && i < here; ++i, at_.next()) ok = chunk(i + 1 < here || have);
             }
             if (!ok) {
-                umma_commit(cx.bar(kDrain));
+                if (leader) umma_commit(cx.bar(kDrain));
                 (void)mbar_wait(cx.bar(kDrain), 0);
             }
         }
@@ -366,66 +460,96 @@ la_chunked_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constan
         while (ok && wk.next(G, p.seg)) {
             const Rows rw = rows_of(G, wk.it, wk.h);
             const uint8_t* mrow = p.mask ? p.mask + (long long)wk.it.bb * G.T + wk.it.bos : nullptr;
-            const float ghead = p.g_per_head ? to_f32(p.g[wk.h]) : 0.f;
-            for (int i = 0; ok && i < wk.chunks; ++i, ++n) {
-                const int st = n % NS, t0 = wk.first_token(i) + 4 * lane;
-                // four tokens a lane: log2 decays, which tokens enter, which rows get outputs
+            const float ghead = p.g_per_head ? clamp_log_decay(to_f32(p.g[wk.h])) : 0.f;
+            // four tokens a lane; the next chunk's are in flight while this one is scanned
+            uint16_t graw[4] = {0, 0, 0, 0};
+            uint8_t mraw[4] = {1, 1, 1, 1};
+            auto fetch = [&](int t0) {
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    const int t = min(t0 + 4 * lane + q, wk.te - 1);
+                    if (!p.g_per_head)
+                        graw[q] = reinterpret_cast<const uint16_t*>(p.g)[rw.first + t * rw.step];
+                    if (mrow) mraw[q] = mrow[t];
+                }
+            };
+            if (wk.chunks > 0) fetch(wk.first_token(0));
+            for (int i = 0; ok && i < wk.chunks; ++i, at_.next()) {
+                const int st = at_.st, t0 = wk.first_token(i) + 4 * lane;
+                // log decays, which tokens exist, which update the state
                 float gl[4];
                 uint32_t in = 0, upd = 0;
 #pragma unroll
                 for (int q = 0; q < 4; ++q) {
-                    const int t = t0 + q;
-                    gl[q] = 0.f;
-                    if (t < wk.te) {
-                        in |= 1u << q;
-                        if (!mrow || mrow[t]) {
-                            upd |= 1u << q;
-                            gl[q] = clamp_log_decay(p.g_per_head
-                                                        ? ghead
-                                                        : to_f32(p.g[rw.first + t * rw.step]));
-                        }
-                    }
+                    in |= (t0 + q < wk.te ? 1u : 0u) << q;
+                    upd |= (t0 + q < wk.te && mraw[q] ? 1u : 0u) << q;
+                    const float x =
+                        p.g_per_head ? ghead
+                                     : clamp_log_decay(__uint_as_float((uint32_t)graw[q] << 16));
+                    gl[q] = (upd >> q) & 1 ? x : 0.f;
                 }
-                double c[4];
-                c[0] = gl[0];
-                c[1] = c[0] + gl[1];
-                c[2] = c[1] + gl[2];
-                c[3] = c[2] + gl[3];
-                double inc = c[3];
+                if (i + 1 < wk.chunks) fetch(wk.first_token(i + 1));
+                const uint32_t enter = kRev ? in : upd, outs = kRev ? upd : in;
+                // Sums inside a 32-token block (8 lanes): `far` from the token to its border
+                // (the tokens after it; backward in time the ones from the block's second
+                // to it), summed in that direction, so that it is as exact as it is
+                // small; and inclusive prefix sums c.
+                const float own = (gl[0] + gl[1]) + (gl[2] + gl[3]);
+                float pre = own, far_l = kRev ? ((lane & 7) == 0 ? (gl[1] + gl[2]) + gl[3] : own) : own;
 #pragma unroll
-                for (int m = 1; m < 32; m <<= 1) {
-                    const double o = __shfl_up_sync(0xffffffffu, inc, m);
-                    if (lane >= m) inc += o;
+                for (int m = 1; m < 8; m <<= 1) {
+                    const float a = __shfl_up_sync(0xffffffffu, pre, m, 8);
+                    const float b = kRev ? __shfl_up_sync(0xffffffffu, far_l, m, 8)
+                                         : __shfl_down_sync(0xffffffffu, far_l, m, 8);
+                    if ((lane & 7) >= m) pre += a;
+                    if (kRev ? (lane & 7) >= m : (lane & 7) + m < 8) far_l += b;
                 }
-                const double pre = inc - c[3];
-                const double tot = __shfl_sync(0xffffffffu, inc, 31);
-                if (n >= NS && !(ok = cx.wait_warp(kEmpty + st, (n / NS - 1) & 1))) break;
-                Scan* sc = scan_of(st);
-                const uint32_t enter = kRev ? in : upd;
-                float cc[4], kf[4];
+                // what lies beyond this lane's four tokens
+                float far_o = kRev ? __shfl_up_sync(0xffffffffu, far_l, 1, 8)
+                                   : __shfl_down_sync(0xffffffffu, far_l, 1, 8);
+                if (kRev ? (lane & 7) == 0 : (lane & 7) == 7) far_o = 0.f;
+                const float t0s = __shfl_sync(0xffffffffu, pre, 7), t1s = __shfl_sync(0xffffffffu, pre, 15),
+                            t2s = __shfl_sync(0xffffffffu, pre, 23), t3s = __shfl_sync(0xffffffffu, pre, 31);
+                const int blk = lane >> 3;
+                const float before = blk == 0 ? 0.f : blk == 1 ? t0s : blk == 2 ? t0s + t1s : t0s + t1s + t2s;
+                const float after = blk == 3 ? 0.f : blk == 2 ? t3s : blk == 1 ? t2s + t3s : t1s + t2s + t3s;
+                float c = before + (pre - own);
+                float cc[4], ff[4];
 #pragma unroll
                 for (int q = 0; q < 4; ++q) {
-                    const double x = pre + c[q];
-                    cc[q] = (float)(x * 1.4426950408889634);
-                    kf[q] = (enter >> q) & 1 ? p.key_scale * expf((float)(kRev ? x : tot - x)) : 0.f;
+                    c += gl[q];
+                    cc[q] = c * kLog2e;
                 }
+                float d = far_o;
+#pragma unroll
+                for (int u = 0; u < 4; ++u) {
+                    const int q = kRev ? u : 3 - u;
+                    if (kRev && !((lane & 7) == 0 && q == 0)) d += gl[q];
+                    ff[q] = (enter >> q) & 1 ? expf(d) : 0.f;
+                    if (!kRev) d += gl[q];
+                }
+                const float tail = __shfl_sync(0xffffffffu, gl[0], lane & 24);  // rev: the border's own
+                if (n >= NS && !(ok = cx.wait_warp(kEmpty + st, at_.ph ^ 1))) break;
+                Scan* sc = scan_of(st);
                 *reinterpret_cast<float4*>(&sc->c[4 * lane]) = make_float4(cc[0], cc[1], cc[2], cc[3]);
-                *reinterpret_cast<float4*>(&sc->k[4 * lane]) = make_float4(kf[0], kf[1], kf[2], kf[3]);
+                *reinterpret_cast<float4*>(&sc->f[4 * lane]) = make_float4(ff[0], ff[1], ff[2], ff[3]);
                 // 8 lanes make a 32-token word
-                uint32_t lw = enter << (4 * (lane & 7)), ow = (kRev ? upd : in) << (4 * (lane & 7));
+                uint32_t lw = enter << (4 * (lane & 7)), ow = outs << (4 * (lane & 7));
 #pragma unroll
                 for (int m = 1; m < 8; m <<= 1) {
                     lw |= __shfl_xor_sync(0xffffffffu, lw, m);
                     ow |= __shfl_xor_sync(0xffffffffu, ow, m);
                 }
                 if ((lane & 7) == 0) {
-                    sc->live[lane >> 3] = lw;
-                    sc->out[lane >> 3] = ow;
+                    sc->live[blk] = lw;
+                    sc->out[blk] = ow;
+                    sc->kb[blk] = p.key_scale * expf(kRev ? before + tail : after);
                 }
-                if (lane == 0) sc->decay = (float)exp(tot);
+                // (1 + the small difference: a constant decay's rounding repeats every chunk)
+                if (lane == 0) sc->decay = 1.f + expm1f((t0s + t1s) + (t2s + t3s));
                 // rows of Z that do not enter may hold anything (0 * NaN is NaN): clear them
                 if (__any_sync(0xffffffffu, enter != 15u)) {
-                    if (!(ok = cx.wait_warp(kFull + st, (n / NS) & 1))) break;
+                    if (!(ok = cx.wait_warp(kFull + st, at_.ph))) break;
                     const uint32_t z = cx.sbase + st * C::kStage + 2 * C::kTile;
                     for (int q = 0; q < 4; ++q) {
                         if ((enter >> q) & 1) continue;
@@ -445,9 +569,9 @@ la_chunked_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constan
         if (!kStateOnly && lane == 0) {
             bool ok = true;
             while (ok && wk.next(G, p.seg)) {
-                for (int i = 0; ok && i < wk.chunks; ++i, ++n) {
-                    const int st = n % NS, t0 = wk.first_token(i);
-                    if (!(ok = cx.wait(kStore + st, (n / NS) & 1))) break;
+                for (int i = 0; ok && i < wk.chunks; ++i, at_.next()) {
+                    const int st = at_.st, t0 = wk.first_token(i);
+                    if (!(ok = cx.wait(kStore + st, at_.ph))) break;
                     if (t0 + kChunk <= wk.te) {
                         const uint32_t at = cx.sbase + st * C::kStage + 2 * C::kTile;
                         const At a = tma_row(G, wk.it, wk.h, t0);
@@ -469,47 +593,54 @@ la_chunked_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constan
         const int w = warp & 3, row = 32 * w + lane;
         const uint32_t tp = tmem + ((uint32_t)(32 * w) << 16) + C::TM_P;
         while (!kStateOnly && ok && wk.next(G, p.seg)) {
-            for (int i = 0; ok && i < wk.chunks; ++i, ++n) {
-                const int st = n % NS;
-                if (!(ok = cx.wait_warp(kScan + st, (n / NS) & 1))) break;
+            for (int i = 0; ok && i < wk.chunks; ++i, at_.next()) {
+                const int st = at_.st;
+                if (!(ok = cx.wait_warp(kScan + st, at_.ph))) break;
                 const Scan* sc = scan_of(st);
                 const float ct = sc->c[row];
-                if (!(ok = cx.wait_warp(kScore + (n & 1), (n >> 1) & 1))) break;
+                if (!(ok = cx.wait_warp(kScore + (n & 1), at_.pair()))) break;
                 tc_fence_after();
-#pragma unroll
+                // Loops stay rolled: four roles share the instruction cache of each
+                // sub-partition, and one warp running long straight code is fetch-bound.
+#pragma unroll 1
                 for (int b = 0; b < 4; ++b) {
                     uint32_t out[16];
-                    const bool none = kRev ? b < w : b > w;
-                    if (none) {
+                    const uint32_t live = sc->live[b];
+                    if (kRev ? b < w : b > w) {
 #pragma unroll
                         for (int q = 0; q < 16; ++q) out[q] = 0;
+                    } else if (b != w && live == 0xffffffffu) {
+                        // token to its block's border to this row: both exponents <= 0
+                        const float border = sc->c[kRev ? 32 * b : 32 * b + 31];
+                        const float r = p.pair_scale * ex2(kRev ? border - ct : ct - border);
+                        float v[32];
+                        tmem_ld32(tp + 32 * b, v);
+                        tmem_ld_wait();
+#pragma unroll
+                        for (int q = 0; q < 32; q += 4) {
+                            const float4 f = *reinterpret_cast<const float4*>(&sc->f[32 * b + q]);
+                            out[q / 2] = pack_bf16(v[q] * r * f.x, v[q + 1] * r * f.y);
+                            out[q / 2 + 1] = pack_bf16(v[q + 2] * r * f.z, v[q + 3] * r * f.w);
+                        }
                     } else {
-                        const uint32_t live = sc->live[b];
-                        // keys that this row may use: live, and on the diagonal block not
+                        // keys that this row may use: live and, on the diagonal block, not
                         // on the wrong side of the row
                         uint32_t use = live;
                         if (b == w) use &= kRev ? 0xffffffffu << lane : 0xffffffffu >> (31 - lane);
+                        float v[32];
+                        tmem_ld32(tp + 32 * b, v);
+                        tmem_ld_wait();
 #pragma unroll
-                        for (int half = 0; half < 2; ++half) {
-                            float v[16];
-                            tmem_ld16(tp + 32 * b + 16 * half, v);
-                            tmem_ld_wait();
+                        for (int q = 0; q < 32; q += 4) {
+                            const float4 c = *reinterpret_cast<const float4*>(&sc->c[32 * b + q]);
+                            const float c4[4] = {c.x, c.y, c.z, c.w};
 #pragma unroll
-                            for (int q = 0; q < 16; q += 4) {
-                                const float4 cs =
-                                    *reinterpret_cast<const float4*>(&sc->c[32 * b + 16 * half + q]);
-                                const float c4[4] = {cs.x, cs.y, cs.z, cs.w};
-#pragma unroll
-                                for (int u = 0; u < 4; ++u) {
-                                    const float e = ex2(kRev ? c4[u] - ct : ct - c4[u]);
-                                    v[q + u] = (use >> (16 * half + q + u)) & 1
-                                                   ? v[q + u] * p.pair_scale * e
-                                                   : 0.f;
-                                }
+                            for (int u = 0; u < 4; ++u) {
+                                const float e = ex2(kRev ? c4[u] - ct : ct - c4[u]);
+                                v[q + u] = (use >> (q + u)) & 1 ? v[q + u] * p.pair_scale * e : 0.f;
                             }
-#pragma unroll
-                            for (int q = 0; q < 8; ++q)
-                                out[8 * half + q] = pack_bf16(v[2 * q], v[2 * q + 1]);
+                            out[q / 2] = pack_bf16(v[q], v[q + 1]);
+                            out[q / 2 + 1] = pack_bf16(v[q + 2], v[q + 3]);
                         }
                     }
                     // in place: block b's 16 columns lie over scores that are read already
@@ -538,55 +669,37 @@ la_chunked_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constan
         float S[R];
         const uint32_t state_s = cx.sbase + C::OFF_STATE;
         // entries (2 m, 2 m + 1) at D = 64: row srow + 8 (m & 1), columns scol + 8 (m / 2) ..
+        auto entry = [&](int q, int rs, int cs) {  // offset of entry q for row and column strides
+            return kBoth ? srow * rs + (scol + q) * cs
+                         : (srow + 8 * ((q >> 1) & 1)) * rs + (scol + 8 * (q >> 2) + (q & 1)) * cs;
+        };
         auto load_state = [&](const float* s, bool transposed) {
-            if constexpr (kBoth) {
-                if (!transposed) {
+            constexpr int V = kBoth ? 4 : 2;  // neighbouring columns a thread holds
+            if (!transposed) {
 #pragma unroll
-                    for (int q = 0; q < R; q += 4) {
-                        const float4 x = *reinterpret_cast<const float4*>(s + srow * D + scol + q);
+                for (int q = 0; q < R; q += V) {
+                    const float* src = s + entry(q, D, 1);
+                    if constexpr (kBoth) {
+                        const float4 x = *reinterpret_cast<const float4*>(src);
                         S[q] = x.x; S[q + 1] = x.y; S[q + 2] = x.z; S[q + 3] = x.w;
+                    } else {
+                        const float2 x = *reinterpret_cast<const float2*>(src);
+                        S[q] = x.x; S[q + 1] = x.y;
                     }
-                } else {
-#pragma unroll
-                    for (int q = 0; q < R; ++q) S[q] = s[(scol + q) * D + srow];
                 }
             } else {
 #pragma unroll
-                for (int m = 0; m < R / 2; ++m) {
-                    const int r = srow + 8 * (m & 1), c = scol + 8 * (m / 2);
-                    if (!transposed) {
-                        const float2 x = *reinterpret_cast<const float2*>(s + r * D + c);
-                        S[2 * m] = x.x;
-                        S[2 * m + 1] = x.y;
-                    } else {
-                        S[2 * m] = s[c * D + r];
-                        S[2 * m + 1] = s[(c + 1) * D + r];
-                    }
-                }
+                for (int q = 0; q < R; ++q) S[q] = s[entry(q, 1, D)];
             }
         };
-        auto save_state = [&](float* s, bool transposed) {
-            if constexpr (kBoth) {
-                if (!transposed) {
+        auto save_state = [&](float* s) {
 #pragma unroll
-                    for (int q = 0; q < R; q += 4)
-                        *reinterpret_cast<float4*>(s + srow * D + scol + q) =
-                            make_float4(S[q], S[q + 1], S[q + 2], S[q + 3]);
-                } else {
-#pragma unroll
-                    for (int q = 0; q < R; ++q) s[(scol + q) * D + srow] = S[q];
-                }
-            } else {
-#pragma unroll
-                for (int m = 0; m < R / 2; ++m) {
-                    const int r = srow + 8 * (m & 1), c = scol + 8 * (m / 2);
-                    if (!transposed) {
-                        *reinterpret_cast<float2*>(s + r * D + c) = make_float2(S[2 * m], S[2 * m + 1]);
-                    } else {
-                        s[c * D + r] = S[2 * m];
-                        s[(c + 1) * D + r] = S[2 * m + 1];
-                    }
-                }
+            for (int q = 0; q < R; q += kBoth ? 4 : 2) {
+                float* dst = s + entry(q, D, 1);
+                if constexpr (kBoth)
+                    *reinterpret_cast<float4*>(dst) = make_float4(S[q], S[q + 1], S[q + 2], S[q + 3]);
+                else
+                    *reinterpret_cast<float2*>(dst) = make_float2(S[q], S[q + 1]);
             }
         };
         // U0 in bf16, [row][column] with the columns in 64-wide swizzled blocks
@@ -617,7 +730,7 @@ la_chunked_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constan
         const bool works = has_state || !kStateOnly;
         while (ok && works && wk.next(G, p.seg)) {
             const long long state_at = ((long long)wk.it.n * G.H + wk.h) * D * D;
-            const long long seg_at = (wk.slot * G.H + wk.h) * D * D;
+            const long long seg_at = ((long long)wk.slot * G.H + wk.h) * D * D;
             const Rows rw = rows_of(G, wk.it, wk.h);
             if (has_state) {
                 if (!kStateOnly && p.init) {
@@ -627,15 +740,15 @@ la_chunked_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constan
                     for (int q = 0; q < R; ++q) S[q] = 0.f;
                 }
             }
-            double logs = 0.0;
+            float logs = 0.f;
             if (has_state && wk.chunks > 0) publish_state();
-            for (int i = 0; ok && i < wk.chunks; ++i, ++n) {
-                const int st = n % NS, t0 = wk.first_token(i);
+            for (int i = 0; ok && i < wk.chunks; ++i, at_.next()) {
+                const int st = at_.st, t0 = wk.first_token(i);
                 const uint32_t x = cx.sbase + st * C::kStage, y = x + C::kTile, z = y + C::kTile;
-                if (!(ok = cx.wait_warp(kScan + st, (n / NS) & 1))) break;
+                if (!(ok = cx.wait_warp(kScan + st, at_.ph))) break;
                 const Scan* sc = scan_of(st);
                 const float decay = sc->decay;
-                if (kStateOnly) logs += (double)sc->c[127];
+                if (kStateOnly) logs += sc->c[127];
                 float rowf = 0.f;
                 bool row_out = true;
                 if (!kStateOnly && !first) {
@@ -649,7 +762,7 @@ la_chunked_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constan
                 // decays with t as it should (with the exact G_end the rounding of all terms
                 // would stay in dg of tokens that G_end no longer reaches).
                 if (kRev && !kStateOnly && p.ck_dot && has_state) {
-                    const long long u = slot_of(G, wk.it, t0 / kChunk, kChunk) * G.H + wk.h;
+                    const long long u = wk.unit(G, t0);
                     const float4* ck = static_cast<const float4*>(p.ck) + u * (D * D / 4) + sthread;
                     float s = 0.f;
 #pragma unroll
@@ -668,36 +781,46 @@ la_chunked_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constan
                 }
 
                 if (first) {  // k . Y in two parts
-                    if (!(ok = cx.wait_warp(kFull + st, (n / NS) & 1))) break;
-                    if (!kStateOnly && !(ok = cx.wait_warp(kScore + (n & 1), (n >> 1) & 1))) break;
-                    if (!kStateOnly && C::kLoInX && !(ok = cx.wait_warp(kCross + (n & 1), (n >> 1) & 1)))
+                    if (!(ok = cx.wait_warp(kFull + st, at_.ph))) break;
+                    if (!kStateOnly && !(ok = cx.wait_warp(kScore + (n & 1), at_.pair()))) break;
+                    if (!kStateOnly && C::kPartsInPlace && !(ok = cx.wait_warp(kCross + (n & 1), at_.pair())))
                         break;
-                    const uint32_t lo = C::kLoInX ? x : cx.sbase + C::OFF_LO;
-#pragma unroll 4
+                    const uint32_t part1 = C::kPartsInPlace ? x : cx.sbase + C::OFF_PARTS;
+                    const uint32_t part2 = C::kPartsInPlace ? state_s : part1 + C::kTile;
+                    const bool fine = p.parts > 1;
+#pragma unroll 1
                     for (int u = 0; u < D / 8; ++u) {
                         const int idx = u * 128 + wt;
                         const uint32_t at = (idx >> 10) * C::kSub + (idx & 1023) * 16;
-                        const float f = sc->k[(idx & 1023) >> 3];
+                        const int row = (idx & 1023) >> 3;
+                        const float f = sc->f[row] * sc->kb[row >> 5];
                         const uint4 v = ld_shared16(y + at);
                         const uint32_t in[4] = {v.x, v.y, v.z, v.w};
-                        uint32_t hi[4], lw[4];
+                        uint32_t h[4], m[4], l[4];
 #pragma unroll
                         for (int q = 0; q < 4; ++q) {
-                            const float a = __uint_as_float(in[q] << 16) * f;
-                            const float b = __uint_as_float(in[q] & 0xffff0000u) * f;
-                            hi[q] = pack_bf16(a, b);
-                            lw[q] = pack_bf16(a - __uint_as_float(hi[q] << 16),
-                                              b - __uint_as_float(hi[q] & 0xffff0000u));
-                            if (f == 0.f) hi[q] = lw[q] = 0;  // whatever the row holds
+                            float a = __uint_as_float(in[q] << 16) * f;
+                            float b = __uint_as_float(in[q] & 0xffff0000u) * f;
+                            if (f == 0.f) a = b = 0.f;  // whatever the row holds
+                            h[q] = pack_bf16(a, b);
+                            a -= __uint_as_float(h[q] << 16);
+                            b -= __uint_as_float(h[q] & 0xffff0000u);
+                            m[q] = pack_bf16(a, b);
+                            a -= __uint_as_float(m[q] << 16);
+                            b -= __uint_as_float(m[q] & 0xffff0000u);
+                            l[q] = pack_bf16(a, b);
                         }
-                        st_shared16(y + at, hi[0], hi[1], hi[2], hi[3]);
-                        st_shared16(lo + at, lw[0], lw[1], lw[2], lw[3]);
+                        st_shared16(y + at, h[0], h[1], h[2], h[3]);
+                        if (fine) {
+                            st_shared16(part1 + at, m[0], m[1], m[2], m[3]);
+                            st_shared16(part2 + at, l[0], l[1], l[2], l[3]);
+                        }
                     }
                     fence_proxy_async();
                     cx.arrive(kKReady);
                 }
 
-                if (!(ok = cx.wait_warp(kDelta, n & 1))) break;
+                if (!(ok = cx.wait_warp(kDelta, at_.odd()))) break;
                 tc_fence_after();
                 if (has_state) {
                     if constexpr (kBoth) {
@@ -721,7 +844,7 @@ la_chunked_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constan
                     }
                     // forward: keep the state at the chunk's end
                     if (!kRev && !kStateOnly && p.ck) {
-                        const long long u = slot_of(G, wk.it, t0 / kChunk, kChunk) * G.H + wk.h;
+                        const long long u = wk.unit(G, t0);
                         float4* ck = static_cast<float4*>(p.ck) + u * (D * D / 4) + sthread;
 #pragma unroll
                         for (int q = 0; q < R / 4; ++q)
@@ -739,7 +862,7 @@ la_chunked_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constan
                     const long long grow = rw.first + (long long)t * rw.step;
                     const uint32_t to = tmem + ((uint32_t)(32 * w) << 16);
                     float dot = 0.f;
-#pragma unroll
+#pragma unroll 1
                     for (int q = 0; q < D; q += 16) {
                         float ox[16], oi[16];
                         tmem_ld16(to + C::TM_OX + q, ox);
@@ -792,11 +915,11 @@ la_chunked_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constan
             if (!ok) break;
             if (has_state) {
                 if (kStateOnly) {
-                    save_state(p.seg_state + seg_at, p.init_transposed);
+                    save_state(p.seg_state + seg_at);
                     if (sthread == 0)
-                        p.seg_decay[wk.slot * G.H + wk.h] = (float)exp2(logs);
+                        p.seg_decay[(long long)wk.slot * G.H + wk.h] = ex2(logs);
                 } else if (p.fin && (kRev ? wk.it.j == 0 : wk.it.j == wk.it.nseg - 1)) {
-                    save_state(p.fin + state_at, p.init_transposed);
+                    save_state(p.fin + state_at);
                 }
             }
         }

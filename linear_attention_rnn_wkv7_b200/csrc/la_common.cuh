@@ -137,11 +137,13 @@ struct Pass {
     float pair_scale;     // on y_t z_t^T inside out (the score part)
     float inter_scale;    // on what the state before the chunk gives to out
     float key_scale;      // on y_t z_t^T inside the state
+    int parts;            // bf16 parts of the state update's operand (tensor cores): 3 where the
+                          // state itself is a result, 1 where it only makes bf16 results
     int seg;              // tokens per segment (a multiple of kChunk)
     const float* init;    // states before the first token: [N][H][D][D], or by slot when
     int init_by_slot;     // init_by_slot; nullptr: zeros
-    int init_transposed;  // init (and fin) hold [z][y] instead of [y][z]
-    float* fin;           // final states [N][H][D][D], or nullptr
+    int init_transposed;  // init holds [z][y] instead of [y][z]
+    float* fin;           // final states [N][H][D][D] as [y][z], or nullptr
     // state-only passes: each segment's own state and e^{sum of g}
     float* seg_state;     // [slot][H][D][D]
     float* seg_decay;     // [slot][H]

@@ -150,6 +150,7 @@ inline cudaError_t forward(const Problem& p, const Tin* q, const Tin* k, const T
     a.out = o;
     a.pair_scale = a.inter_scale = scale;
     a.key_scale = 1.f;
+    a.parts = sT || plan.split ? 3 : 1;
     a.seg = plan.seg;
     a.init = s0;
     a.fin = sT;
@@ -175,10 +176,13 @@ inline cudaError_t backward(const Problem& p, const Tin* q, const Tin* k, const 
     f.g = g;
     f.g_per_head = g_per_head;
     f.mask = mask;
+    // dq's kept states meet sums of their own terms in dg, whose difference counts
+    f.parts = plan.split ? 3 : dg ? 2 : 1;
     f.seg = plan.seg;
     Pass<Tin> r = f;  // against it
     r.pair_scale = r.key_scale = scale;
     r.inter_scale = 1.f;
+    r.parts = ds0 || plan.split ? 3 : 1;
     f.pair_scale = f.inter_scale = scale;
     f.key_scale = 1.f;
     f.init = s0;
@@ -187,6 +191,7 @@ inline cudaError_t backward(const Problem& p, const Tin* q, const Tin* k, const 
         Pass<Tin> a = f;
         a.y = k;
         a.z = v;
+        a.parts = 3;
         cudaError_t e = run_segments<Tin, false>(a, p, s0, ws, b.fwd, stream);
         if (e != cudaSuccess) return e;
         a = r;
@@ -222,6 +227,7 @@ inline cudaError_t backward(const Problem& p, const Tin* q, const Tin* k, const 
     a.x = v;
     a.y = dout;
     a.z = q;
+    a.parts = 1;  // its state is no result
     a.out = dk;
     a.init_transposed = 1;
     if (dg) {

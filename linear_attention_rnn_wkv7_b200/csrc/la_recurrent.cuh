@@ -55,24 +55,9 @@ __device__ __forceinline__ void load_tile(const float* s, bool transposed, int r
     }
 }
 template <int D>
-__device__ __forceinline__ void store_tile(float* s, bool transposed, int row0, int col0,
-                                           const float4 (&S)[16]) {
-    if (!transposed) {
+__device__ __forceinline__ void store_tile(float* s, int row0, int col0, const float4 (&S)[16]) {
 #pragma unroll
-        for (int i = 0; i < 16; ++i) *reinterpret_cast<float4*>(s + (row0 + i) * D + col0) = S[i];
-    } else {
-#pragma unroll
-        for (int i = 0; i < 16; i += 4) {
-            float* p = s + col0 * D + row0 + i;
-            *reinterpret_cast<float4*>(p) = make_float4(S[i].x, S[i + 1].x, S[i + 2].x, S[i + 3].x);
-            *reinterpret_cast<float4*>(p + D) =
-                make_float4(S[i].y, S[i + 1].y, S[i + 2].y, S[i + 3].y);
-            *reinterpret_cast<float4*>(p + 2 * D) =
-                make_float4(S[i].z, S[i + 1].z, S[i + 2].z, S[i + 3].z);
-            *reinterpret_cast<float4*>(p + 3 * D) =
-                make_float4(S[i].w, S[i + 1].w, S[i + 2].w, S[i + 3].w);
-        }
-    }
+    for (int i = 0; i < 16; ++i) *reinterpret_cast<float4*>(s + (row0 + i) * D + col0) = S[i];
 }
 
 template <typename Tin, int D, bool kRev, bool kStateOnly>
@@ -343,10 +328,10 @@ la_recurrent_kernel(const Pass<Tin> p) {
         }
     }
     if (kStateOnly) {
-        store_tile<D>(p.seg_state + (slot * G.H + h) * D * D, p.init_transposed, row0, col0, S);
+        store_tile<D>(p.seg_state + (slot * G.H + h) * D * D, row0, col0, S);
         if (tid == 0 && slab == 0) p.seg_decay[slot * G.H + h] = (float)exp(logtot);
     } else if (p.fin && (kRev ? it.j == 0 : it.j == it.nseg - 1)) {
-        store_tile<D>(p.fin + state_at, p.init_transposed, row0, col0, S);
+        store_tile<D>(p.fin + state_at, row0, col0, S);
     }
 }
 
