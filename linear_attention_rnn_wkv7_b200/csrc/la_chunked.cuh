@@ -28,9 +28,9 @@
 //     warp 2       decays: prefix sums (64-bit), factors; clears Z's unused rows
 //     warp 3       output tiles shared -> HBM, frees the stage
 //     warps 4-7    P: scores -> E . scores in bf16, in place in tensor memory
-//     warps 8-11   k . Y in two parts over Y (and over X, or a tile of its own);
-//                  the state (all of it at D = 64, half the columns at 128)
-//     warps 12-15  out = f . Ox + Oi; the other half of the state at D = 128
+//     warps 8-11   half of k . Y in parts; the state (at D = 128 half its columns)
+//     warps 12-15  out = f . Ox + Oi; at D = 64 the other half of k . Y, at D = 128 (where
+//                  warps 4-7 make that) the other half of the state
 // The chain from one chunk to the next is only U0 -> bf16 -> (Ox, dU) -> U1; the state never
 // goes through tensor memory.  All waits are on mbarriers and bounded (a second); a thread that
 // gives up sets a flag that ends every other wait, so the CTA always reaches its end, waits
@@ -40,6 +40,7 @@
 #include <cuda.h>
 
 #include <atomic>
+#include <type_traits>
 
 #include "chunked.cuh"
 #include "la_common.cuh"
@@ -62,19 +63,21 @@ struct Cfg {
     static constexpr int kStage = 3 * kTile;
     static constexpr int kStateSub = D * 128;         // D rows of 64 bf16
     static constexpr int kStateBytes = (D / 64) * kStateSub;
-    // The second and third part of k . Y: over X and over U0's copy once their products are
-    // done, or (where there is room) in tiles of their own, which takes that wait off the
-    // chain.
-    static constexpr bool kPartsInPlace = D == 128;
+    // D = 64: k . Y is made a chunk ahead, its second and third part in tiles of their own (two
+    // sets), and P and dU are double in tensor memory, so that only the state itself ties a
+    // chunk to the next.  D = 128 has room for neither: the parts lie over X and over U0's
+    // copy once their products are done.
+    static constexpr bool kAhead = D == 64;
+    static constexpr bool kPartsInPlace = !kAhead;
     static constexpr int kStateWarps = D == 64 ? 4 : 8;
     static constexpr int OFF_STATE = kStages * kStage;
     static constexpr int OFF_PARTS = OFF_STATE + kStateBytes;
-    static constexpr int OFF_SC = OFF_PARTS + (kPartsInPlace ? 0 : 2 * kTile);
+    static constexpr int OFF_SC = OFF_PARTS + (kPartsInPlace ? 0 : 4 * kTile);
     static constexpr int kScBytes = 2 * 512 + 64;     // struct Scan
     static constexpr int OFF_BAR = OFF_SC + kStages * kScBytes;
     static constexpr int kBytes = OFF_BAR + 256;
     // tensor memory columns
-    static constexpr int TM_P = 0, TM_OI = 128, TM_OX = 128 + D, TM_DU = 128 + 2 * D;
+    static constexpr int TM_P = 0, TM_OI = kAhead ? 256 : 128, TM_OX = TM_OI + D, TM_DU = TM_OX + D;
 };
 
 // One stage's decays.  Tokens come in blocks of 32; a block's border is its last token
@@ -86,7 +89,8 @@ struct Scan {
     uint32_t live[4];  // tokens that enter as keys
     uint32_t out[4];   // rows that get an output (others are written as 0)
     float decay;       // e^{c_L}
-    float pad[3];
+    int more;          // another chunk follows in this CTA
+    float pad[2];
 };
 static_assert(sizeof(Scan) == 1088, "kScBytes");
 
@@ -114,6 +118,34 @@ __device__ __forceinline__ uint4 ld_shared16(uint32_t addr) {
                  : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
                  : "r"(addr));
     return v;
+}
+// Two fp32 operations in one instruction (a register pair).
+__device__ __forceinline__ uint64_t pair2(float a, float b) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ void split2(uint64_t x, float& a, float& b) {
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(x));
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+// The bf16 pair of two fp32, and back.
+__device__ __forceinline__ uint32_t pack2(uint64_t x) {
+    float a, b;
+    split2(x, a, b);
+    return pack_bf16(a, b);
+}
+__device__ __forceinline__ uint64_t unpack2(uint32_t x) {
+    return pair2(__uint_as_float(x << 16), __uint_as_float(x & 0xffff0000u));
 }
 // 32 lanes x 32 columns: thread i gets lane i's.
 __device__ __forceinline__ void tmem_ld32(uint32_t taddr, float (&v)[32]) {
@@ -165,13 +197,14 @@ enum Bar {
     kStore = 12,   // [4] a stage's output tile is in shared memory
     kScore = 16,   // [2] P = X Y^T is done
     kCross = 18,   // [2] Ox = X U0 is done
-    kPReady = 20,  // P in bf16 is in tensor memory
-    kKReady = 21,  // k . Y is in shared memory
-    kSReady = 22,  // U0 in bf16 is in shared memory (and the last dU has been read)
-    kDelta = 23,   // dU is done, and with it every product of the chunk
-    kOFree = 24,   // Ox and Oi have been read
-    kDrain = 25,   // after an abort: all MMAs are done
-    kBars = 26
+    kPReady = 20,  // [2] P in bf16 is in tensor memory
+    kKReady = 22,  // [2] k . Y is in shared memory
+    kDelta = 24,   // [2] dU is done
+    kSReady = 26,  // U0 in bf16 is in shared memory (and the last dU has been read)
+    kOut = 27,     // Ox, Oi and every other product of the chunk are done
+    kOFree = 28,   // Ox and Oi have been read
+    kDrain = 29,   // after an abort: all MMAs are done
+    kBars = 30
 };
 
 // The slow path of a wait, kept out of line (the roles' code has to fit the instruction
@@ -313,7 +346,8 @@ la_chunked_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constan
         for (int i = 0; i < kBars; ++i) {
             const int count = i >= kEmpty && i < kEmpty + 4 ? (kStateOnly ? 32 * C::kStateWarps : 1)
                               : i >= kStore && i < kStore + 4 ? 128
-                              : i == kPReady || i == kKReady || i == kOFree ? 128
+                              : i == kPReady || i == kPReady + 1 || i == kOFree ? 128
+                              : i == kKReady || i == kKReady + 1 ? 256
                               : i == kSReady ? 32 * C::kStateWarps
                                              : 1;
             mbar_init(cx.bar(i), count);
@@ -331,6 +365,61 @@ la_chunked_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constan
     Walk<kRev, kStateOnly> wk(G, p.seg);
     Place<NS> at_;
     int& n = at_.n;
+
+    // k . Y of one chunk, in bf16 parts: the first over Y itself.  Two groups of four warps take
+    // half of it each: of the rows at D = 64, of the columns at D = 128.
+    auto scale_keys = [&](const Place<NS>& at, int half) {
+        const int st = at.st;
+        if (!cx.wait_warp(kScan + st, at.ph)) return false;
+        if (!cx.wait_warp(kFull + st, at.ph)) return false;
+        if (!kStateOnly && !cx.wait_warp(kScore + (at.n & 1), at.pair())) return false;
+        if (C::kPartsInPlace) {
+            // X and U0's copy have been read; without them, the last chunk's parts
+            if (!kStateOnly && !cx.wait_warp(kCross + (at.n & 1), at.pair())) return false;
+            if (kStateOnly && at.n > 0 &&
+                !cx.wait_warp(kDelta + ((at.n - 1) & 1), ((at.n - 1) >> 1) & 1))
+                return false;
+        }
+        const Scan* sc = scan_of(st);
+        const uint32_t x = cx.sbase + st * C::kStage, y = x + C::kTile;
+        const uint32_t part1 =
+            C::kPartsInPlace ? x : cx.sbase + C::OFF_PARTS + 2 * C::kTile * (at.n & 1);
+        const uint32_t part2 = C::kPartsInPlace ? cx.sbase + C::OFF_STATE : part1 + C::kTile;
+#pragma unroll 1
+        for (int u = 0; u < D / 16; ++u) {
+            const int idx = (D == 64 ? half * 512 : 0) + u * 128 + (tid & 127), row = idx >> 3;
+            const uint32_t o = (D == 64 ? 0 : half * C::kSub) + idx * 16;
+            const float f = sc->f[row] * sc->kb[row >> 5];
+            uint4 v = ld_shared16(y + o);
+            if (f == 0.f) v = make_uint4(0, 0, 0, 0);  // whatever the row holds
+            const uint64_t ff = pair2(f, f), minus = pair2(-1.f, -1.f);
+            const uint32_t in[4] = {v.x, v.y, v.z, v.w};
+            uint64_t a[4];
+            uint32_t w[4];
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                a[q] = mul2(unpack2(in[q]), ff);
+                w[q] = pack2(a[q]);
+            }
+            st_shared16(y + o, w[0], w[1], w[2], w[3]);
+            if (p.parts > 1) {
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    a[q] = fma2(unpack2(w[q]), minus, a[q]);
+                    w[q] = pack2(a[q]);
+                }
+                st_shared16(part1 + o, w[0], w[1], w[2], w[3]);
+            }
+            if (p.parts > 2) {
+#pragma unroll
+                for (int q = 0; q < 4; ++q) w[q] = pack2(fma2(unpack2(w[q]), minus, a[q]));
+                st_shared16(part2 + o, w[0], w[1], w[2], w[3]);
+            }
+        }
+        fence_proxy_async();
+        cx.arrive(kKReady + (at.n & 1));
+        return true;
+    };
 
     // ------------------------------------------------------------------ warp 0: loads
     if (warp == 0) {
@@ -381,11 +470,12 @@ la_chunked_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constan
                 sc_at.next();
                 tc_fence_after();
                 uint64_t a = kmaj + ((cx.sbase + st * C::kStage) >> 4), b = a + (C::kTile >> 4);
+                const uint32_t tp = tmem + C::TM_P + (C::kAhead ? 128 * (m & 1) : 0);
 #pragma unroll 1
                 for (int s = 0; s < D / 64; ++s) {
 #pragma unroll
                     for (int kk = 0; kk < 4; ++kk)
-                        if (leader) umma_bf16(tmem + C::TM_P, a + 2 * kk, b + 2 * kk, id_score, s + kk > 0);
+                        if (leader) umma_bf16(tp, a + 2 * kk, b + 2 * kk, id_score, s + kk > 0);
                     a += C::kSub >> 4;
                     b += C::kSub >> 4;
                 }
@@ -396,6 +486,31 @@ la_chunked_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constan
                 const int st = at_.st;
                 const uint32_t x = (cx.sbase + st * C::kStage) >> 4, y = x + (C::kTile >> 4),
                                z = y + (C::kTile >> 4), state = (cx.sbase + C::OFF_STATE) >> 4;
+                auto delta = [&]() {  // dU, from the parts of k . Y
+                    if (!cx.wait_warp(kKReady + (n & 1), at_.pair())) return false;
+                    tc_fence_after();
+                    const uint32_t own =
+                        (cx.sbase + C::OFF_PARTS + 2 * C::kTile * (n & 1)) >> 4;
+                    const uint32_t td = tmem + C::TM_DU + (C::kAhead ? 64 * (n & 1) : 0);
+#pragma unroll 1
+                    for (int part = 0; part < p.parts; ++part) {
+                        const uint64_t a =
+                            mn_tile + (part == 0          ? y
+                                       : C::kPartsInPlace ? (part == 1 ? x : state)
+                                                          : own + (part - 1) * (C::kTile >> 4));
+#pragma unroll
+                        for (int kk = 0; kk < 8; ++kk)
+                            if (leader)
+                                umma_bf16(td, a + 128 * kk, mn_tile + z + 128 * kk, id_delta,
+                                          part + kk > 0);
+                    }
+                    if (leader) umma_commit(cx.bar(kDelta + (n & 1)));
+                    return true;
+                };
+                if (C::kAhead && !kStateOnly) {
+                    if (more && !score()) return false;
+                    if (!delta()) return false;  // (its last user's dU was read before U0 came)
+                }
                 if (!cx.wait_warp(kSReady, at_.odd())) return false;
                 if (!kStateOnly) {
                     if (n > 0 && !cx.wait_warp(kOFree, at_.odd() ^ 1)) return false;
@@ -405,37 +520,24 @@ la_chunked_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constan
                     for (int s = 0; s < D / 64; ++s) {
 #pragma unroll
                         for (int kk = 0; kk < 4; ++kk)
-                            if (leader) umma_bf16(tmem + C::TM_OX, a + 2 * kk, b + 128 * kk, id_out, s + kk > 0);
+                            if (leader)
+                                umma_bf16(tmem + C::TM_OX, a + 2 * kk, b + 128 * kk, id_out, s + kk > 0);
                         a += C::kSub >> 4;
                         b += 512;
                     }
-                    if (C::kPartsInPlace && leader) umma_commit(cx.bar(kCross + (n & 1)));
-                    if (!cx.wait_warp(kPReady, at_.odd())) return false;
+                    if (leader) umma_commit(cx.bar(kCross + (n & 1)));
+                    if (!cx.wait_warp(kPReady + (n & 1), at_.pair())) return false;
                     if (!cx.wait_warp(kScan + st, at_.ph)) return false;  // Z's rows are clear
                     tc_fence_after();
                     b = mn_tile + z;
+                    const uint32_t tp = tmem + C::TM_P + (C::kAhead ? 128 * (n & 1) : 0);
 #pragma unroll
                     for (int kk = 0; kk < 8; ++kk)
-                        if (leader) umma_bf16_ts(tmem + C::TM_OI, tmem + C::TM_P + 8 * kk, b + 128 * kk, id_out,
-                                     kk > 0);
-                    if (more && !score()) return false;
+                        if (leader) umma_bf16_ts(tmem + C::TM_OI, tp + 8 * kk, b + 128 * kk, id_out, kk > 0);
+                    if (!C::kAhead && more && !score()) return false;
                 }
-                if (!cx.wait_warp(kKReady, at_.odd())) return false;
-                tc_fence_after();
-                // the parts of k . Y: over Y, and over X and U0 or in their own tiles
-                const uint32_t own = (cx.sbase + C::OFF_PARTS) >> 4;
-#pragma unroll 1
-                for (int part = 0; part < p.parts; ++part) {
-                    const uint64_t a =
-                        mn_tile + (part == 0             ? y
-                                   : C::kPartsInPlace    ? (part == 1 ? x : state)
-                                                         : own + (part - 1) * (C::kTile >> 4));
-#pragma unroll
-                    for (int kk = 0; kk < 8; ++kk)
-                        if (leader) umma_bf16(tmem + C::TM_DU, a + 128 * kk, mn_tile + z + 128 * kk, id_delta,
-                                  part + kk > 0);
-                }
-                if (leader) umma_commit(cx.bar(kDelta));
+                if ((!C::kAhead || kStateOnly) && !delta()) return false;
+                if (leader) umma_commit(cx.bar(kOut));
                 return true;
             };
             // chunks left in this and later segments decide whether another score follows
@@ -457,9 +559,16 @@ la_chunked_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constan
     // ------------------------------------------------------------------ warp 2: decays
     else if (warp == 2) {
         bool ok = true;
-        while (ok && wk.next(G, p.seg)) {
+        auto next_tokens = [&]() {  // the next segment with tokens
+            bool have = wk.next(G, p.seg);
+            while (have && wk.chunks == 0) have = wk.next(G, p.seg);
+            return have;
+        };
+        bool have = next_tokens();
+        while (ok && have) {
             const Rows rw = rows_of(G, wk.it, wk.h);
             const uint8_t* mrow = p.mask ? p.mask + (long long)wk.it.bb * G.T + wk.it.bos : nullptr;
+            const int te = wk.te, chunks = wk.chunks;
             const float ghead = p.g_per_head ? clamp_log_decay(to_f32(p.g[wk.h])) : 0.f;
             // four tokens a lane; the next chunk's are in flight while this one is scanned
             uint16_t graw[4] = {0, 0, 0, 0};
@@ -467,28 +576,31 @@ la_chunked_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constan
             auto fetch = [&](int t0) {
 #pragma unroll
                 for (int q = 0; q < 4; ++q) {
-                    const int t = min(t0 + 4 * lane + q, wk.te - 1);
+                    const int t = min(t0 + 4 * lane + q, te - 1);
                     if (!p.g_per_head)
                         graw[q] = reinterpret_cast<const uint16_t*>(p.g)[rw.first + t * rw.step];
                     if (mrow) mraw[q] = mrow[t];
                 }
             };
-            if (wk.chunks > 0) fetch(wk.first_token(0));
-            for (int i = 0; ok && i < wk.chunks; ++i, at_.next()) {
+            if (chunks > 0) fetch(wk.first_token(0));
+            for (int i = 0; ok && i < chunks; ++i, at_.next()) {
                 const int st = at_.st, t0 = wk.first_token(i) + 4 * lane;
                 // log decays, which tokens exist, which update the state
                 float gl[4];
                 uint32_t in = 0, upd = 0;
 #pragma unroll
                 for (int q = 0; q < 4; ++q) {
-                    in |= (t0 + q < wk.te ? 1u : 0u) << q;
-                    upd |= (t0 + q < wk.te && mraw[q] ? 1u : 0u) << q;
+                    in |= (t0 + q < te ? 1u : 0u) << q;
+                    upd |= (t0 + q < te && mraw[q] ? 1u : 0u) << q;
                     const float x =
                         p.g_per_head ? ghead
                                      : clamp_log_decay(__uint_as_float((uint32_t)graw[q] << 16));
                     gl[q] = (upd >> q) & 1 ? x : 0.f;
                 }
-                if (i + 1 < wk.chunks) fetch(wk.first_token(i + 1));
+                if (i + 1 < chunks)
+                    fetch(wk.first_token(i + 1));
+                else
+                    have = next_tokens();
                 const uint32_t enter = kRev ? in : upd, outs = kRev ? upd : in;
                 // Sums inside a 32-token block (8 lanes): `far` from the token to its border
                 // (the tokens after it; backward in time the ones from the block's second
@@ -546,7 +658,10 @@ la_chunked_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constan
                     sc->kb[blk] = p.key_scale * expf(kRev ? before + tail : after);
                 }
                 // (1 + the small difference: a constant decay's rounding repeats every chunk)
-                if (lane == 0) sc->decay = 1.f + expm1f((t0s + t1s) + (t2s + t3s));
+                if (lane == 0) {
+                    sc->more = i + 1 < chunks || have;
+                    sc->decay = 1.f + expm1f((t0s + t1s) + (t2s + t3s));
+                }
                 // rows of Z that do not enter may hold anything (0 * NaN is NaN): clear them
                 if (__any_sync(0xffffffffu, enter != 15u)) {
                     if (!(ok = cx.wait_warp(kFull + st, at_.ph))) break;
@@ -591,10 +706,15 @@ la_chunked_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constan
     else if (warp < 8) {
         bool ok = true;
         const int w = warp & 3, row = 32 * w + lane;
-        const uint32_t tp = tmem + ((uint32_t)(32 * w) << 16) + C::TM_P;
-        while (!kStateOnly && ok && wk.next(G, p.seg)) {
+        while ((!kStateOnly || C::kPartsInPlace) && ok && wk.next(G, p.seg)) {
             for (int i = 0; ok && i < wk.chunks; ++i, at_.next()) {
                 const int st = at_.st;
+                if (kStateOnly) {
+                    ok = scale_keys(at_, 0);
+                    continue;
+                }
+                const uint32_t tp = tmem + ((uint32_t)(32 * w) << 16) + C::TM_P +
+                                    (C::kAhead ? 128 * (n & 1) : 0);
                 if (!(ok = cx.wait_warp(kScan + st, at_.ph))) break;
                 const Scan* sc = scan_of(st);
                 const float ct = sc->c[row];
@@ -616,11 +736,13 @@ la_chunked_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constan
                         float v[32];
                         tmem_ld32(tp + 32 * b, v);
                         tmem_ld_wait();
+                        const uint64_t rr = pair2(r, r);
 #pragma unroll
                         for (int q = 0; q < 32; q += 4) {
-                            const float4 f = *reinterpret_cast<const float4*>(&sc->f[32 * b + q]);
-                            out[q / 2] = pack_bf16(v[q] * r * f.x, v[q + 1] * r * f.y);
-                            out[q / 2 + 1] = pack_bf16(v[q + 2] * r * f.z, v[q + 3] * r * f.w);
+                            const ulonglong2 f =
+                                *reinterpret_cast<const ulonglong2*>(&sc->f[32 * b + q]);
+                            out[q / 2] = pack2(mul2(mul2(pair2(v[q], v[q + 1]), rr), f.x));
+                            out[q / 2 + 1] = pack2(mul2(mul2(pair2(v[q + 2], v[q + 3]), rr), f.y));
                         }
                     } else {
                         // keys that this row may use: live and, on the diagonal block, not
@@ -630,17 +752,18 @@ la_chunked_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constan
                         float v[32];
                         tmem_ld32(tp + 32 * b, v);
                         tmem_ld_wait();
+                        const uint64_t sign = kRev ? pair2(1.f, 1.f) : pair2(-1.f, -1.f);
+                        const uint64_t cc = kRev ? pair2(-ct, -ct) : pair2(ct, ct);
+                        const uint64_t ps = pair2(p.pair_scale, p.pair_scale);
 #pragma unroll
-                        for (int q = 0; q < 32; q += 4) {
-                            const float4 c = *reinterpret_cast<const float4*>(&sc->c[32 * b + q]);
-                            const float c4[4] = {c.x, c.y, c.z, c.w};
-#pragma unroll
-                            for (int u = 0; u < 4; ++u) {
-                                const float e = ex2(kRev ? c4[u] - ct : ct - c4[u]);
-                                v[q + u] = (use >> (q + u)) & 1 ? v[q + u] * p.pair_scale * e : 0.f;
-                            }
-                            out[q / 2] = pack_bf16(v[q], v[q + 1]);
-                            out[q / 2 + 1] = pack_bf16(v[q + 2], v[q + 3]);
+                        for (int q = 0; q < 32; q += 2) {
+                            const uint64_t c2 =
+                                *reinterpret_cast<const uint64_t*>(&sc->c[32 * b + q]);
+                            float ea, eb, a, d;
+                            split2(fma2(c2, sign, cc), ea, eb);
+                            split2(mul2(mul2(pair2(v[q], v[q + 1]), ps), pair2(ex2(ea), ex2(eb))), a, d);
+                            out[q / 2] =
+                                pack_bf16((use >> q) & 1 ? a : 0.f, (use >> (q + 1)) & 1 ? d : 0.f);
                         }
                     }
                     // in place: block b's 16 columns lie over scores that are read already
@@ -648,17 +771,19 @@ la_chunked_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constan
                 }
                 tmem_st_wait();
                 tc_fence_before();
-                cx.arrive(kPReady);
+                cx.arrive(kPReady + (n & 1));
+                if (C::kPartsInPlace) ok = scale_keys(at_, 0);
             }
         }
     }
     // -------------------------------------- warps 8-15: k . Y and state, outputs and state
     else {
+      auto role = [&](auto which) {
+        constexpr bool first = decltype(which)::value;  // warps 8-11
         bool ok = true;
-        const bool first = warp < 12;      // warps 8-11
         const int w = warp & 3, wt = tid & 127;
         constexpr bool kBoth = D == 128;   // warps 12-15 hold state columns 64..127
-        const bool has_state = first || kBoth;
+        constexpr bool has_state = first || kBoth;
         constexpr int R = D == 64 ? 32 : 64;  // state entries per thread
         const int sthread = first ? wt : 128 + wt;
         constexpr int kSThreads = 32 * C::kStateWarps;
@@ -727,8 +852,10 @@ la_chunked_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constan
             tc_fence_before();
             cx.arrive(kSReady);
         };
-        const bool works = has_state || !kStateOnly;
-        while (ok && works && wk.next(G, p.seg)) {
+        Place<NS> keys;
+        float decay = 0.f, next_decay = 0.f;
+        int more = 0, next_more = 0;
+        while (ok && wk.next(G, p.seg)) {
             const long long state_at = ((long long)wk.it.n * G.H + wk.h) * D * D;
             const long long seg_at = ((long long)wk.slot * G.H + wk.h) * D * D;
             const Rows rw = rows_of(G, wk.it, wk.h);
@@ -741,13 +868,18 @@ la_chunked_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constan
                 }
             }
             float logs = 0.f;
-            if (has_state && wk.chunks > 0) publish_state();
             for (int i = 0; ok && i < wk.chunks; ++i, at_.next()) {
                 const int st = at_.st, t0 = wk.first_token(i);
-                const uint32_t x = cx.sbase + st * C::kStage, y = x + C::kTile, z = y + C::kTile;
-                if (!(ok = cx.wait_warp(kScan + st, at_.ph))) break;
+                const uint32_t z = cx.sbase + st * C::kStage + 2 * C::kTile;
+                // What the state's warps need of a stage's decays they read before they give
+                // that chunk's U0: from then on the stage may be used up and refilled.
+                if (!C::kAhead || n == 0) {
+                    if (!(ok = cx.wait_warp(kScan + st, at_.ph))) break;
+                    decay = scan_of(st)->decay;
+                    more = scan_of(st)->more;
+                }
+                if (i == 0 && has_state) publish_state();
                 const Scan* sc = scan_of(st);
-                const float decay = sc->decay;
                 if (kStateOnly) logs += sc->c[127];
                 float rowf = 0.f;
                 bool row_out = true;
@@ -756,6 +888,24 @@ la_chunked_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constan
                     rowf = p.inter_scale * ex2(kRev ? sc->c[127] - sc->c[row] : sc->c[row]);
                     row_out = (sc->out[w] >> lane) & 1;
                 }
+                // k . Y: of the next chunk where there is room for two (half of it here, half
+                // there), of this one with warps 4-7 otherwise
+                if (C::kAhead) {
+                    if (n == 0) {
+                        ok = scale_keys(keys, first ? 0 : 1);
+                        keys.next();
+                    }
+                    if (ok && more) {
+                        ok = scale_keys(keys, first ? 0 : 1);
+                        next_decay = scan_of(keys.st)->decay;
+                        next_more = scan_of(keys.st)->more;
+                        keys.next();
+                    }
+                } else if (first) {
+                    ok = scale_keys(at_, 1);
+                }
+                if (!ok) break;
+
                 // Backward in time: <S_end, G_end> of the chunk, with G_end rounded as the
                 // product X U0 reads it.  What tokens s >= t take from it in dL/dc is then
                 // the same sum's own terms, and the difference, e^{c_L - c_t} <S_t, G_end>,
@@ -780,47 +930,8 @@ la_chunked_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constan
                     if (lane == 0) p.ck_dot[u * C::kStateWarps + (sthread >> 5)] = s;
                 }
 
-                if (first) {  // k . Y in two parts
-                    if (!(ok = cx.wait_warp(kFull + st, at_.ph))) break;
-                    if (!kStateOnly && !(ok = cx.wait_warp(kScore + (n & 1), at_.pair()))) break;
-                    if (!kStateOnly && C::kPartsInPlace && !(ok = cx.wait_warp(kCross + (n & 1), at_.pair())))
-                        break;
-                    const uint32_t part1 = C::kPartsInPlace ? x : cx.sbase + C::OFF_PARTS;
-                    const uint32_t part2 = C::kPartsInPlace ? state_s : part1 + C::kTile;
-                    const bool fine = p.parts > 1;
-#pragma unroll 1
-                    for (int u = 0; u < D / 8; ++u) {
-                        const int idx = u * 128 + wt;
-                        const uint32_t at = (idx >> 10) * C::kSub + (idx & 1023) * 16;
-                        const int row = (idx & 1023) >> 3;
-                        const float f = sc->f[row] * sc->kb[row >> 5];
-                        const uint4 v = ld_shared16(y + at);
-                        const uint32_t in[4] = {v.x, v.y, v.z, v.w};
-                        uint32_t h[4], m[4], l[4];
-#pragma unroll
-                        for (int q = 0; q < 4; ++q) {
-                            float a = __uint_as_float(in[q] << 16) * f;
-                            float b = __uint_as_float(in[q] & 0xffff0000u) * f;
-                            if (f == 0.f) a = b = 0.f;  // whatever the row holds
-                            h[q] = pack_bf16(a, b);
-                            a -= __uint_as_float(h[q] << 16);
-                            b -= __uint_as_float(h[q] & 0xffff0000u);
-                            m[q] = pack_bf16(a, b);
-                            a -= __uint_as_float(m[q] << 16);
-                            b -= __uint_as_float(m[q] & 0xffff0000u);
-                            l[q] = pack_bf16(a, b);
-                        }
-                        st_shared16(y + at, h[0], h[1], h[2], h[3]);
-                        if (fine) {
-                            st_shared16(part1 + at, m[0], m[1], m[2], m[3]);
-                            st_shared16(part2 + at, l[0], l[1], l[2], l[3]);
-                        }
-                    }
-                    fence_proxy_async();
-                    cx.arrive(kKReady);
-                }
-
-                if (!(ok = cx.wait_warp(kDelta, at_.odd()))) break;
+                // (without a state here: for the next chunk's parts' sake)
+                if (!(ok = cx.wait_warp(kDelta + (n & 1), at_.pair()))) break;
                 tc_fence_after();
                 if (has_state) {
                     if constexpr (kBoth) {
@@ -836,7 +947,7 @@ la_chunked_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constan
 #pragma unroll
                         for (int q = 0; q < R; q += 16) {
                             float d[16];
-                            tmem_ld16x32(tmem + ((uint32_t)(32 * w) << 16) + C::TM_DU + 2 * q, d);
+                            tmem_ld16x32(tmem + ((uint32_t)(32 * w) << 16) + C::TM_DU + 64 * (n & 1) + 2 * q, d);
                             tmem_ld_wait();
 #pragma unroll
                             for (int u = 0; u < 16; ++u) S[q + u] = fmaf(decay, S[q + u], d[u]);
@@ -851,58 +962,77 @@ la_chunked_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constan
                             ck[q * kSThreads] =
                                 make_float4(S[4 * q], S[4 * q + 1], S[4 * q + 2], S[4 * q + 3]);
                     }
-                    // the next chunk's U0 (every product that reads the last one is done)
+                    // the next chunk's U0, once the product that reads this one is done
+                    if (C::kAhead && !kStateOnly &&
+                        !(ok = cx.wait_warp(kCross + (n & 1), at_.pair())))
+                        break;
                     if (i + 1 < wk.chunks) publish_state();
                     if (kStateOnly) cx.arrive(kEmpty + st);
                 }
+                if (C::kAhead) {
+                    decay = next_decay;
+                    more = next_more;
+                }
 
                 if (!kStateOnly && !first) {  // outputs
+                    if (!(ok = cx.wait_warp(kOut, at_.odd()))) break;
+                    tc_fence_after();
                     const int row = 32 * w + lane, t = t0 + row;
                     const bool in = t < wk.te, whole = t0 + kChunk <= wk.te;
                     const long long grow = rw.first + (long long)t * rw.step;
                     const uint32_t to = tmem + ((uint32_t)(32 * w) << 16);
                     float dot = 0.f;
+                    // 32 columns at a time where registers allow (no state beside them)
+                    constexpr int V = kBoth ? 16 : 32;
 #pragma unroll 1
-                    for (int q = 0; q < D; q += 16) {
-                        float ox[16], oi[16];
-                        tmem_ld16(to + C::TM_OX + q, ox);
-                        tmem_ld16(to + C::TM_OI + q, oi);
-                        uint4 wv[2];
+                    for (int q = 0; q < D; q += V) {
+                        float ox[V], oi[V];
+                        if constexpr (kBoth) {
+                            tmem_ld16(to + C::TM_OX + q, ox);
+                            tmem_ld16(to + C::TM_OI + q, oi);
+                        } else {
+                            tmem_ld32(to + C::TM_OX + q, ox);
+                            tmem_ld32(to + C::TM_OI + q, oi);
+                        }
+                        uint4 wv[V / 8];
                         if (p.dots && in && row_out) {
                             const uint4* src =
                                 reinterpret_cast<const uint4*>(p.dot_with + grow * D + q);
-                            wv[0] = src[0];
-                            wv[1] = src[1];
+#pragma unroll
+                            for (int u = 0; u < V / 8; ++u) wv[u] = src[u];
                         }
                         tmem_ld_wait();
-                        uint32_t pk[8];
 #pragma unroll
-                        for (int u = 0; u < 16; ++u) ox[u] = fmaf(rowf, ox[u], oi[u]);
-                        if (!row_out) {
+                        for (int u = 0; u < V; ++u) ox[u] = fmaf(rowf, ox[u], oi[u]);
+                        if (__any_sync(0xffffffffu, !row_out)) {
 #pragma unroll
-                            for (int u = 0; u < 16; ++u) ox[u] = 0.f;
+                            for (int u = 0; u < V; ++u) ox[u] = row_out ? ox[u] : 0.f;
                         }
                         if (p.dots && in && row_out) {
-                            const uint32_t ww[8] = {wv[0].x, wv[0].y, wv[0].z, wv[0].w,
-                                                    wv[1].x, wv[1].y, wv[1].z, wv[1].w};
 #pragma unroll
-                            for (int u = 0; u < 8; ++u) {
-                                dot = fmaf(ox[2 * u], __uint_as_float(ww[u] << 16), dot);
-                                dot = fmaf(ox[2 * u + 1], __uint_as_float(ww[u] & 0xffff0000u), dot);
+                            for (int u = 0; u < V / 8; ++u) {
+                                const uint32_t ww[4] = {wv[u].x, wv[u].y, wv[u].z, wv[u].w};
+#pragma unroll
+                                for (int r = 0; r < 4; ++r) {
+                                    dot = fmaf(ox[8 * u + 2 * r], __uint_as_float(ww[r] << 16), dot);
+                                    dot = fmaf(ox[8 * u + 2 * r + 1],
+                                               __uint_as_float(ww[r] & 0xffff0000u), dot);
+                                }
                             }
                         }
+                        const uint32_t base = z + (q / 64) * C::kSub + row * 128;
+                        uint4* dst = reinterpret_cast<uint4*>(p.out + grow * D + q);
 #pragma unroll
-                        for (int u = 0; u < 8; ++u) pk[u] = pack_bf16(ox[2 * u], ox[2 * u + 1]);
-                        if (whole) {
-                            const uint32_t base = z + (q / 64) * C::kSub + row * 128;
-                            const int c = (q % 64) / 8;
-                            st_shared16(base + ((c ^ (row & 7)) << 4), pk[0], pk[1], pk[2], pk[3]);
-                            st_shared16(base + (((c + 1) ^ (row & 7)) << 4), pk[4], pk[5], pk[6],
-                                        pk[7]);
-                        } else if (in) {
-                            uint4* dst = reinterpret_cast<uint4*>(p.out + grow * D + q);
-                            dst[0] = make_uint4(pk[0], pk[1], pk[2], pk[3]);
-                            dst[1] = make_uint4(pk[4], pk[5], pk[6], pk[7]);
+                        for (int u = 0; u < V / 8; ++u) {
+                            uint32_t pk[4];
+#pragma unroll
+                            for (int r = 0; r < 4; ++r)
+                                pk[r] = pack_bf16(ox[8 * u + 2 * r], ox[8 * u + 2 * r + 1]);
+                            if (whole)
+                                st_shared16(base + ((((q % 64) / 8 + u) ^ (row & 7)) << 4), pk[0], pk[1],
+                                            pk[2], pk[3]);
+                            else if (in)
+                                dst[u] = make_uint4(pk[0], pk[1], pk[2], pk[3]);
                         }
                     }
                     tc_fence_before();
@@ -923,6 +1053,11 @@ la_chunked_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constan
                 }
             }
         }
+      };
+      if (warp < 12)
+          role(std::true_type{});
+      else
+          role(std::false_type{});
     }
     __syncwarp();
     tc_fence_before();

@@ -55,7 +55,7 @@ struct Geom {
         return (long long)N * segs(T, seg);
     }
     __host__ __device__ static int segs(int len, int seg) {
-        return len <= seg ? 1 : (int)(((long long)len + seg - 1) / seg);
+        return len <= seg ? 1 : (len - 1) / seg + 1;
     }
 };
 
@@ -77,12 +77,13 @@ __device__ __forceinline__ bool seqlens_ok(const Geom& g, int tid, int threads) 
     return !__syncthreads_or(bad);
 }
 
-__device__ __forceinline__ Item locate(const Geom& g, long long slot, int seg) {
+// (Slot numbers fit 32 bits: the entry points check.)
+__device__ __forceinline__ Item locate(const Geom& g, int slot, int seg) {
     Item it;
     if (!g.cu) {
         it.nseg = Geom::segs(g.T, seg);
-        it.n = (int)(slot / it.nseg);
-        it.j = (int)(slot - (long long)it.n * it.nseg);
+        it.n = slot / it.nseg;
+        it.j = slot - it.n * it.nseg;
         it.bos = 0;
         it.len = g.T;
         it.bb = it.n;
@@ -91,12 +92,12 @@ __device__ __forceinline__ Item locate(const Geom& g, long long slot, int seg) {
     int lo = 0, hi = g.N;  // the last n with floor(cu[n] / seg) + n <= slot
     while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
-        if ((long long)g.cu[mid] / seg + mid <= slot) lo = mid; else hi = mid;
+        if (g.cu[mid] / seg + mid <= slot) lo = mid; else hi = mid;
     }
     it.n = lo;
     it.bos = g.cu[lo];
     it.len = g.cu[lo + 1] - it.bos;
-    it.j = (int)(slot - it.bos / seg - lo);
+    it.j = slot - it.bos / seg - lo;
     it.nseg = Geom::segs(it.len, seg);
     it.bb = 0;
     if (it.j >= it.nseg) it.n = -1;
@@ -217,7 +218,7 @@ la_dg_kernel(Geom g, const uint8_t* __restrict__ mask, const float* __restrict__
     if (id >= slots * g.H) return;
     const long long slot = id / g.H;
     const int h = (int)(id - slot * g.H);
-    const Item it = locate(g, slot, kC);
+    const Item it = locate(g, (int)slot, kC);
     if (it.n < 0) {
         if (part && lane == 0) part[id] = 0.f;
         return;

@@ -85,7 +85,7 @@ la_recurrent_kernel(const Pass<Tin> p) {
     const long long sh = blockIdx.x / C::kSlabs;
     const int h = (int)(sh % G.H);
     const long long slot = sh / G.H;
-    const Item it = locate(G, slot, p.seg);
+    const Item it = locate(G, (int)slot, p.seg);
     if (it.n < 0) return;
     // a state-only pass runs the segments whose state a later one (in the pass's
     // direction) starts from
