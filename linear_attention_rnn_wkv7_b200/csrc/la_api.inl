@@ -22,7 +22,7 @@ wkv7_status la_problem(wkv7::la::Problem& p, int B, int T, int H, int K, int V, 
     if (algo == WKV7_ALGO_CHUNKED && !la_chunked_ok(K, dtype)) return WKV7_ERR_UNSUPPORTED;
     // grids, TMA coordinates and slot numbers are 32-bit
     const long long units = (long long)N * H, tokens = (long long)B * T;
-    if (tokens > 0x7fffffffLL || units > 0x7fffffffLL / 16 ||
+    if (tokens > 0x7ffffe00LL || units > 0x7fffffffLL / 16 ||
         (tokens / wkv7::la::kRecChunk + 2LL * N + 1) * H * (K / 64) > 0x7fffffffLL ||
         (long long)B * H > 0x7fffffffLL)
         return WKV7_ERR_UNSUPPORTED;

@@ -225,6 +225,21 @@ __device__ __noinline__ bool wait_slow(uint32_t bar, uint32_t parity, volatile i
     return false;
 }
 
+__device__ __noinline__ bool handoff_slow(const unsigned* flag, volatile int* abort) {
+    const uint64_t t0 = globaltimer_ns();
+    for (uint32_t k = 0; k < (1u << 28); ++k) {
+        unsigned v;
+        asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(flag) : "memory");
+        if (v != 0) return true;
+        if (*abort) return false;
+        if (globaltimer_ns() - t0 > 1000000000ull) break;
+        __nanosleep(100);
+    }
+    *abort = 1;
+    raise_flag(4 /* WKV7_ERR_DEVICE_TIMEOUT */);
+    return false;
+}
+
 struct Ctx {
     uint32_t sbase, bars;
     volatile int* abort;
@@ -238,6 +253,10 @@ struct Ctx {
         return __all_sync(0xffffffffu, wait(i, parity));
     }
     __device__ __forceinline__ void arrive(int i) const { mbar_arrive(bar(i)); }
+    // The flag of a state handed on, for a whole warp (bounded as the other waits).
+    __device__ __forceinline__ bool wait_handoff(const unsigned* flag) const {
+        return __all_sync(0xffffffffu, handoff_slow(flag, abort));
+    }
 };
 
 // A role's place in the list of chunks: the n-th of the CTA, in stage st for the ph-th time.
@@ -256,39 +275,101 @@ struct Place {
     __device__ __forceinline__ uint32_t pair() const { return (n >> 1) & 1; }  // two in turn
 };
 
-// The CTA's chunks in order: segments (item) round robin, a segment's chunks in the direction
-// of the pass.  Every role walks the same list.  (Slot and item numbers fit 32 bits: the
-// entry points check.)
-struct Seg {
+// Schedule: which chunks a CTA works on, as pieces (consecutive chunks of one (sequence,
+// head)); every role walks the same list.
+//  - Segments (run == 0): the sequences' segments round robin.  For few (sequence, head)
+//    pairs, whose segments start from states made beforehand, and for passes over states only.
+//  - Runs: all chunks, laid end to end (heads, sequences, chunks in the direction of the
+//    pass), are cut into equal runs, one per CTA, and a CTA takes its run's pieces from the
+//    last to the first.  A sequence cut between CTAs m and m + 1 thus has its first chunks
+//    at the start of m's work and its last ones at the end of m + 1's: the state that m hands
+//    on (through ho_state[m]) is there long before it is needed, unless a sequence is
+//    longer than a run.  A CTA only ever waits for the one before it, so the order in which
+//    blocks start is enough for progress.
+// Without runs 512 sequences of one length on 148 SMs take 4 rounds for 3.46 rounds' work.
+// (Slot and chunk numbers fit 32 bits: the entry points check.)
+struct Piece {
     Item it;
-    int h, slot, tb, te, chunks;  // segment [tb, te) of the sequence
+    int h, slot, tb, te, chunks;  // tokens [tb, te) of the sequence
+    bool begins, ends;            // its first (last) chunk in the direction of the pass is the sequence's
 };
-// The item if it has work (chunks >= 0).  Out of line: divisions, in every role.
-__device__ __noinline__ Seg find_item(const Geom& g, int seg, int item, int rev, int state_only) {
-    Seg s;
+// The segment of that number, if it has work (chunks >= 0).  Out of line: divisions, in
+// every role.
+__device__ __noinline__ Piece find_segment(const Geom& g, int seg, int item, int rev, int state_only) {
+    Piece s;
     s.slot = item / g.H;
     s.h = item - s.slot * g.H;
     s.it = locate(g, s.slot, seg);
     s.tb = s.te = 0;
     s.chunks = -1;
     if (s.it.n < 0) return s;
-    if (state_only && (rev ? s.it.j == 0 : s.it.j == s.it.nseg - 1)) return s;
+    s.begins = rev ? s.it.j == s.it.nseg - 1 : s.it.j == 0;
+    s.ends = rev ? s.it.j == 0 : s.it.j == s.it.nseg - 1;
+    if (state_only && s.ends) return s;
     s.tb = s.it.j * seg;
     s.te = s.it.len - s.tb < seg ? s.it.len : s.tb + seg;
     s.chunks = (s.te - s.tb + kChunk - 1) / kChunk;
     return s;
 }
+// The piece that ends at position pos of a run that starts at `start`; `pos` becomes the position
+// before it.
+__device__ __noinline__ Piece find_piece(const Geom& g, int slots, int start, int& pos, int rev) {
+    Piece s;
+    s.h = pos / slots;
+    const int at = pos - s.h * slots;
+    s.slot = rev ? slots - 1 - at : at;
+    s.it = locate(g, s.slot, kChunk);
+    s.tb = s.te = 0;
+    s.chunks = -1;
+    if (s.it.n < 0) {
+        --pos;
+        return s;
+    }
+    const int total = s.it.nseg;  // chunks [first, last] in the direction of the pass
+    const int last = rev ? total - 1 - s.it.j : s.it.j;
+    const int first = last - (pos - start) > 0 ? last - (pos - start) : 0;
+    s.begins = first == 0;
+    s.ends = last == total - 1;
+    s.tb = kChunk * (rev ? total - 1 - last : first);
+    const int te = kChunk * (rev ? total - first : last + 1);
+    s.te = s.it.len < te ? s.it.len : te;
+    s.chunks = (s.te - s.tb + kChunk - 1) / kChunk;
+    pos -= last - first + 1;
+    return s;
+}
 template <bool kRev, bool kStateOnly>
-struct Walk : Seg {
-    int item, items;
-    __device__ __forceinline__ Walk(const Geom& g, int seg)
-        : item((int)blockIdx.x - (int)gridDim.x), items((int)(g.slots(seg) * g.H)) {}
-    // The next segment that has work; false: none left.
-    __device__ __forceinline__ bool next(const Geom& g, int seg) {
-        while (items - item > (int)gridDim.x) {
-            item += gridDim.x;
-            static_cast<Seg&>(*this) = find_item(g, seg, item, kRev, kStateOnly);
-            if (this->chunks >= 0) return true;
+struct Walk : Piece {
+    int item, items;   // segments; or positions: the next one, the run's first
+    int slots;
+    template <typename P>
+    __device__ __forceinline__ explicit Walk(const P& p) {
+        const Geom& g = p.geom;
+        if (kStateOnly || p.run == 0) {
+            slots = 0;
+            item = (int)blockIdx.x - (int)gridDim.x;
+            items = (int)(g.slots(p.seg) * g.H);
+        } else {
+            slots = (int)g.slots(kChunk);
+            const long long all = (long long)slots * g.H, start = (long long)blockIdx.x * p.run;
+            items = (int)start;
+            item = (int)(start + p.run < all ? start + p.run : all) - 1;
+        }
+    }
+    // The next piece; false: none left.
+    template <typename P>
+    __device__ __forceinline__ bool next(const P& p) {
+        if (kStateOnly || slots == 0) {
+            while (items - item > (int)gridDim.x) {
+                item += gridDim.x;
+                static_cast<Piece&>(*this) =
+                    find_segment(p.geom, p.seg, item, kRev, kStateOnly);
+                if (this->chunks >= 0) return true;
+            }
+        } else {
+            while (item >= items) {
+                static_cast<Piece&>(*this) = find_piece(p.geom, slots, items, item, kRev);
+                if (this->chunks >= 0) return true;
+            }
         }
         return false;
     }
@@ -304,6 +385,56 @@ struct Walk : Seg {
     }
 };
 
+// k . Y for `turns` x 128 groups of 8 elements from group `first` of a 128 x 64 tile, in `parts`
+// bf16 parts (the first in place).  Out of line: one copy for the warps that share it.
+__device__ __noinline__ void split_keys(uint32_t y, uint32_t part1, uint32_t part2, const Scan* sc,
+                                        int first, int turns, int parts) {
+    const uint64_t minus = pair2(-1.f, -1.f);
+#pragma unroll 1
+    for (int u = 0; u < turns; u += 2) {
+        uint64_t a[2][4];
+        uint32_t w[2][4], at[2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int idx = first + (u + h) * 128 + (threadIdx.x & 127), row = idx >> 3;
+            at[h] = idx * 16;
+            const float f = sc->f[row] * sc->kb[row >> 5];
+            uint4 v = ld_shared16(y + at[h]);
+            if (f == 0.f) v = make_uint4(0, 0, 0, 0);  // whatever the row holds
+            const uint64_t ff = pair2(f, f);
+            const uint32_t in[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                a[h][q] = mul2(unpack2(in[q]), ff);
+                w[h][q] = pack2(a[h][q]);
+            }
+        }
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+            st_shared16(y + at[h], w[h][0], w[h][1], w[h][2], w[h][3]);
+        if (parts > 1) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    a[h][q] = fma2(unpack2(w[h][q]), minus, a[h][q]);
+                    w[h][q] = pack2(a[h][q]);
+                }
+                st_shared16(part1 + at[h], w[h][0], w[h][1], w[h][2], w[h][3]);
+            }
+        }
+        if (parts > 2) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+#pragma unroll
+                for (int q = 0; q < 4; ++q)
+                    w[h][q] = pack2(fma2(unpack2(w[h][q]), minus, a[h][q]));
+                st_shared16(part2 + at[h], w[h][0], w[h][1], w[h][2], w[h][3]);
+            }
+        }
+    }
+}
+
 // TMA coordinates (1, 2) of the row of token t.
 struct At {
     int c1, c2;
@@ -313,7 +444,8 @@ __device__ __forceinline__ At tma_row(const Geom& g, const Item& it, int h, int 
     return {h, it.bb * g.T + it.bos + t};
 }
 
-template <int D, bool kRev, bool kStateOnly>
+// kGrad: for dg (states kept or met, dot products of outputs).
+template <int D, bool kRev, bool kStateOnly, bool kGrad>
 __global__ void __launch_bounds__(kThreads, 1)
 la_chunked_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_y,
                   const __grid_constant__ CUtensorMap tm_z,
@@ -362,7 +494,7 @@ la_chunked_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constan
     auto scan_of = [&](int st) {
         return reinterpret_cast<Scan*>(smem + C::OFF_SC + st * C::kScBytes);
     };
-    Walk<kRev, kStateOnly> wk(G, p.seg);
+    Walk<kRev, kStateOnly> wk(p);
     Place<NS> at_;
     int& n = at_.n;
 
@@ -380,42 +512,13 @@ la_chunked_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constan
                 !cx.wait_warp(kDelta + ((at.n - 1) & 1), ((at.n - 1) >> 1) & 1))
                 return false;
         }
-        const Scan* sc = scan_of(st);
         const uint32_t x = cx.sbase + st * C::kStage, y = x + C::kTile;
         const uint32_t part1 =
             C::kPartsInPlace ? x : cx.sbase + C::OFF_PARTS + 2 * C::kTile * (at.n & 1);
         const uint32_t part2 = C::kPartsInPlace ? cx.sbase + C::OFF_STATE : part1 + C::kTile;
-#pragma unroll 1
-        for (int u = 0; u < D / 16; ++u) {
-            const int idx = (D == 64 ? half * 512 : 0) + u * 128 + (tid & 127), row = idx >> 3;
-            const uint32_t o = (D == 64 ? 0 : half * C::kSub) + idx * 16;
-            const float f = sc->f[row] * sc->kb[row >> 5];
-            uint4 v = ld_shared16(y + o);
-            if (f == 0.f) v = make_uint4(0, 0, 0, 0);  // whatever the row holds
-            const uint64_t ff = pair2(f, f), minus = pair2(-1.f, -1.f);
-            const uint32_t in[4] = {v.x, v.y, v.z, v.w};
-            uint64_t a[4];
-            uint32_t w[4];
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                a[q] = mul2(unpack2(in[q]), ff);
-                w[q] = pack2(a[q]);
-            }
-            st_shared16(y + o, w[0], w[1], w[2], w[3]);
-            if (p.parts > 1) {
-#pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    a[q] = fma2(unpack2(w[q]), minus, a[q]);
-                    w[q] = pack2(a[q]);
-                }
-                st_shared16(part1 + o, w[0], w[1], w[2], w[3]);
-            }
-            if (p.parts > 2) {
-#pragma unroll
-                for (int q = 0; q < 4; ++q) w[q] = pack2(fma2(unpack2(w[q]), minus, a[q]));
-                st_shared16(part2 + o, w[0], w[1], w[2], w[3]);
-            }
-        }
+        const uint32_t o = D == 64 ? 0 : half * C::kSub;
+        split_keys(y + o, part1 + o, part2 + o, scan_of(st), D == 64 ? half * 512 : 0, D / 16,
+                   p.parts);
         fence_proxy_async();
         cx.arrive(kKReady + (at.n & 1));
         return true;
@@ -425,7 +528,7 @@ la_chunked_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constan
     if (warp == 0) {
         if (lane == 0) {
             bool ok = true;
-            while (ok && wk.next(G, p.seg)) {
+            while (ok && wk.next(p)) {
                 for (int i = 0; ok && i < wk.chunks; ++i, at_.next()) {
                     const int st = at_.st;
                     if (n >= NS && !(ok = cx.wait(kEmpty + st, at_.ph ^ 1))) break;
@@ -541,13 +644,13 @@ la_chunked_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constan
                 return true;
             };
             // chunks left in this and later segments decide whether another score follows
-            bool have = wk.next(G, p.seg);
-            while (have && wk.chunks == 0) have = wk.next(G, p.seg);
+            bool have = wk.next(p);
+            while (have && wk.chunks == 0) have = wk.next(p);
             if (have && !kStateOnly) ok = score();
             while (ok && have) {
                 const int here = __shfl_sync(0xffffffffu, wk.chunks, 0);
-                have = wk.next(G, p.seg);
-                while (have && wk.chunks == 0) have = wk.next(G, p.seg);
+                have = wk.next(p);
+                while (have && wk.chunks == 0) have = wk.next(p);
                 for (int i = 0; ok && i < here; ++i, at_.next()) ok = chunk(i + 1 < here || have);
             }
             if (!ok) {
@@ -560,8 +663,8 @@ la_chunked_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constan
     else if (warp == 2) {
         bool ok = true;
         auto next_tokens = [&]() {  // the next segment with tokens
-            bool have = wk.next(G, p.seg);
-            while (have && wk.chunks == 0) have = wk.next(G, p.seg);
+            bool have = wk.next(p);
+            while (have && wk.chunks == 0) have = wk.next(p);
             return have;
         };
         bool have = next_tokens();
@@ -681,32 +784,45 @@ la_chunked_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constan
     }
     // ------------------------------------------------------------------ warp 3: stores
     else if (warp == 3) {
-        if (!kStateOnly && lane == 0) {
+        if (!kStateOnly) {
             bool ok = true;
-            while (ok && wk.next(G, p.seg)) {
+            while (ok && wk.next(p)) {
+                const Rows rw = rows_of(G, wk.it, wk.h);
                 for (int i = 0; ok && i < wk.chunks; ++i, at_.next()) {
                     const int st = at_.st, t0 = wk.first_token(i);
-                    if (!(ok = cx.wait(kStore + st, at_.ph))) break;
+                    if (!(ok = cx.wait_warp(kStore + st, at_.ph))) break;
+                    const uint32_t tile = cx.sbase + st * C::kStage + 2 * C::kTile;
                     if (t0 + kChunk <= wk.te) {
-                        const uint32_t at = cx.sbase + st * C::kStage + 2 * C::kTile;
-                        const At a = tma_row(G, wk.it, wk.h, t0);
+                        if (lane == 0) {
+                            const At a = tma_row(G, wk.it, wk.h, t0);
 #pragma unroll
-                        for (int s = 0; s < D / 64; ++s)
-                            tma_store_3d(&tm_out, at + s * C::kSub, 64 * s, a.c1, a.c2);
-                        bulk_commit();
-                        bulk_wait_read0();
+                            for (int s = 0; s < D / 64; ++s)
+                                tma_store_3d(&tm_out, tile + s * C::kSub, 64 * s, a.c1, a.c2);
+                            bulk_commit();
+                            bulk_wait_read0();
+                        }
+                    } else {  // the sequence's last rows: those behind it belong to others
+                        for (int e = lane; e < (wk.te - t0) * (D / 8); e += 32) {
+                            const int row = e / (D / 8), c = e % (D / 8);
+                            const uint4 v = ld_shared16(tile + (c / 8) * C::kSub + row * 128 +
+                                                        (((c % 8) ^ (row & 7)) << 4));
+                            *reinterpret_cast<uint4*>(
+                                p.out + (rw.first + (long long)(t0 + row) * rw.step) * D + 8 * c) = v;
+                        }
+                        fence_proxy_async();  // the stage's next copy comes behind these reads
                     }
-                    cx.arrive(kEmpty + st);
+                    __syncwarp();
+                    if (lane == 0) cx.arrive(kEmpty + st);
                 }
             }
-            bulk_wait0();
+            if (lane == 0) bulk_wait0();
         }
     }
     // ------------------------------------------------------------------ warps 4-7: P
     else if (warp < 8) {
         bool ok = true;
         const int w = warp & 3, row = 32 * w + lane;
-        while ((!kStateOnly || C::kPartsInPlace) && ok && wk.next(G, p.seg)) {
+        while ((!kStateOnly || C::kPartsInPlace) && ok && wk.next(p)) {
             for (int i = 0; ok && i < wk.chunks; ++i, at_.next()) {
                 const int st = at_.st;
                 if (kStateOnly) {
@@ -855,12 +971,22 @@ la_chunked_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constan
         Place<NS> keys;
         float decay = 0.f, next_decay = 0.f;
         int more = 0, next_more = 0;
-        while (ok && wk.next(G, p.seg)) {
+        while (ok && wk.next(p)) {
             const long long state_at = ((long long)wk.it.n * G.H + wk.h) * D * D;
             const long long seg_at = ((long long)wk.slot * G.H + wk.h) * D * D;
             const Rows rw = rows_of(G, wk.it, wk.h);
             if (has_state) {
-                if (!kStateOnly && p.init) {
+                if (!kStateOnly && p.run > 0 && !wk.begins) {  // handed on by the CTA before
+                    const int from = (int)blockIdx.x - 1;
+                    if (!(ok = cx.wait_handoff(p.ho_flag + 8 * from + (sthread >> 5)))) break;
+                    const float4* src =
+                        reinterpret_cast<const float4*>(p.ho_state + (long long)from * D * D) + sthread;
+#pragma unroll
+                    for (int q = 0; q < R / 4; ++q) {
+                        const float4 x = __ldcg(src + q * kSThreads);
+                        S[4 * q] = x.x; S[4 * q + 1] = x.y; S[4 * q + 2] = x.z; S[4 * q + 3] = x.w;
+                    }
+                } else if (!kStateOnly && p.init) {
                     load_state(p.init + (p.init_by_slot ? seg_at : state_at), p.init_transposed);
                 } else {
 #pragma unroll
@@ -878,7 +1004,7 @@ la_chunked_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constan
                     decay = scan_of(st)->decay;
                     more = scan_of(st)->more;
                 }
-                if (i == 0 && has_state) publish_state();
+                if (has_state && (C::kAhead || i == 0)) publish_state();
                 const Scan* sc = scan_of(st);
                 if (kStateOnly) logs += sc->c[127];
                 float rowf = 0.f;
@@ -891,11 +1017,7 @@ la_chunked_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constan
                 // k . Y: of the next chunk where there is room for two (half of it here, half
                 // there), of this one with warps 4-7 otherwise
                 if (C::kAhead) {
-                    if (n == 0) {
-                        ok = scale_keys(keys, first ? 0 : 1);
-                        keys.next();
-                    }
-                    if (ok && more) {
+                    for (int k = n == 0 ? 0 : 1; ok && k < 1 + (more ? 1 : 0); ++k) {
                         ok = scale_keys(keys, first ? 0 : 1);
                         next_decay = scan_of(keys.st)->decay;
                         next_more = scan_of(keys.st)->more;
@@ -911,7 +1033,7 @@ la_chunked_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constan
                 // the same sum's own terms, and the difference, e^{c_L - c_t} <S_t, G_end>,
                 // decays with t as it should (with the exact G_end the rounding of all terms
                 // would stay in dg of tokens that G_end no longer reaches).
-                if (kRev && !kStateOnly && p.ck_dot && has_state) {
+                if (kGrad && kRev && has_state) {
                     const long long u = wk.unit(G, t0);
                     const float4* ck = static_cast<const float4*>(p.ck) + u * (D * D / 4) + sthread;
                     float s = 0.f;
@@ -954,7 +1076,7 @@ la_chunked_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constan
                         }
                     }
                     // forward: keep the state at the chunk's end
-                    if (!kRev && !kStateOnly && p.ck) {
+                    if (kGrad && !kRev) {
                         const long long u = wk.unit(G, t0);
                         float4* ck = static_cast<float4*>(p.ck) + u * (D * D / 4) + sthread;
 #pragma unroll
@@ -966,7 +1088,7 @@ la_chunked_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constan
                     if (C::kAhead && !kStateOnly &&
                         !(ok = cx.wait_warp(kCross + (n & 1), at_.pair())))
                         break;
-                    if (i + 1 < wk.chunks) publish_state();
+                    if (!C::kAhead && i + 1 < wk.chunks) publish_state();  // (before any output)
                     if (kStateOnly) cx.arrive(kEmpty + st);
                 }
                 if (C::kAhead) {
@@ -978,7 +1100,7 @@ la_chunked_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constan
                     if (!(ok = cx.wait_warp(kOut, at_.odd()))) break;
                     tc_fence_after();
                     const int row = 32 * w + lane, t = t0 + row;
-                    const bool in = t < wk.te, whole = t0 + kChunk <= wk.te;
+                    const bool in = t < wk.te;
                     const long long grow = rw.first + (long long)t * rw.step;
                     const uint32_t to = tmem + ((uint32_t)(32 * w) << 16);
                     float dot = 0.f;
@@ -995,7 +1117,7 @@ la_chunked_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constan
                             tmem_ld32(to + C::TM_OI + q, oi);
                         }
                         uint4 wv[V / 8];
-                        if (p.dots && in && row_out) {
+                        if (kGrad && in && row_out) {
                             const uint4* src =
                                 reinterpret_cast<const uint4*>(p.dot_with + grow * D + q);
 #pragma unroll
@@ -1008,7 +1130,7 @@ la_chunked_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constan
 #pragma unroll
                             for (int u = 0; u < V; ++u) ox[u] = row_out ? ox[u] : 0.f;
                         }
-                        if (p.dots && in && row_out) {
+                        if (kGrad && in && row_out) {
 #pragma unroll
                             for (int u = 0; u < V / 8; ++u) {
                                 const uint32_t ww[4] = {wv[u].x, wv[u].y, wv[u].z, wv[u].w};
@@ -1021,23 +1143,19 @@ la_chunked_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constan
                             }
                         }
                         const uint32_t base = z + (q / 64) * C::kSub + row * 128;
-                        uint4* dst = reinterpret_cast<uint4*>(p.out + grow * D + q);
 #pragma unroll
                         for (int u = 0; u < V / 8; ++u) {
                             uint32_t pk[4];
 #pragma unroll
                             for (int r = 0; r < 4; ++r)
                                 pk[r] = pack_bf16(ox[8 * u + 2 * r], ox[8 * u + 2 * r + 1]);
-                            if (whole)
-                                st_shared16(base + ((((q % 64) / 8 + u) ^ (row & 7)) << 4), pk[0], pk[1],
-                                            pk[2], pk[3]);
-                            else if (in)
-                                dst[u] = make_uint4(pk[0], pk[1], pk[2], pk[3]);
+                            st_shared16(base + ((((q % 64) / 8 + u) ^ (row & 7)) << 4), pk[0], pk[1],
+                                        pk[2], pk[3]);
                         }
                     }
                     tc_fence_before();
                     cx.arrive(kOFree);
-                    if (p.dots && in) p.dots[grow] = dot;
+                    if (kGrad && in) p.dots[grow] = dot;
                     fence_proxy_async();
                     cx.arrive(kStore + st);
                 }
@@ -1048,8 +1166,23 @@ la_chunked_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constan
                     save_state(p.seg_state + seg_at);
                     if (sthread == 0)
                         p.seg_decay[(long long)wk.slot * G.H + wk.h] = ex2(logs);
-                } else if (p.fin && (kRev ? wk.it.j == 0 : wk.it.j == wk.it.nseg - 1)) {
-                    save_state(p.fin + state_at);
+                } else if (wk.ends) {
+                    if (p.fin) save_state(p.fin + state_at);
+                } else if (p.run > 0) {
+                    float4* dst =
+                        reinterpret_cast<float4*>(p.ho_state + (long long)blockIdx.x * D * D) + sthread;
+#pragma unroll
+                    for (int q = 0; q < R / 4; ++q)
+                        __stcg(dst + q * kSThreads,
+                               make_float4(S[4 * q], S[4 * q + 1], S[4 * q + 2], S[4 * q + 3]));
+                    // each warp hands its own entries to the same warp of the next CTA
+                    __threadfence();
+                    __syncwarp();
+                    if (lane == 0)
+                        asm volatile("st.release.gpu.global.u32 [%0], %1;" ::"l"(
+                                         p.ho_flag + 8 * (int)blockIdx.x + (sthread >> 5)),
+                                     "r"(1u)
+                                     : "memory");
                 }
             }
         }
@@ -1088,7 +1221,7 @@ inline bool make_map(CUtensorMap* map, const void* ptr, int B, const Geom& g, in
 }
 
 // SMs of the current device and the kernel's shared-memory size, set once per device.
-template <int D, bool kRev, bool kStateOnly>
+template <int D, bool kRev, bool kStateOnly, bool kGrad>
 inline int prepare_device() {
     constexpr int kMaxDev = 64;
     static std::atomic<int> sms[kMaxDev];
@@ -1096,7 +1229,7 @@ inline int prepare_device() {
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDev) return 0;
     int n = sms[dev].load(std::memory_order_acquire);
     if (n > 0) return n;
-    if (cudaFuncSetAttribute(la_chunked_kernel<D, kRev, kStateOnly>,
+    if (cudaFuncSetAttribute(la_chunked_kernel<D, kRev, kStateOnly, kGrad>,
                              cudaFuncAttributeMaxDynamicSharedMemorySize,
                              Cfg<D>::kBytes) != cudaSuccess ||
         cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
@@ -1105,9 +1238,9 @@ inline int prepare_device() {
     return n;
 }
 
-template <int D, bool kRev, bool kStateOnly>
+template <int D, bool kRev, bool kStateOnly, bool kGrad>
 inline cudaError_t launch_d(const Pass<__nv_bfloat16>& p, int B, cudaStream_t stream) {
-    const int sms = prepare_device<D, kRev, kStateOnly>();
+    const int sms = prepare_device<D, kRev, kStateOnly, kGrad>();
     if (sms <= 0) {
         const cudaError_t e = cudaGetLastError();
         return e != cudaSuccess ? e : cudaErrorInvalidDevice;
@@ -1116,16 +1249,24 @@ inline cudaError_t launch_d(const Pass<__nv_bfloat16>& p, int B, cudaStream_t st
     const void* ptr[4] = {kStateOnly ? p.y : p.x, p.y, p.z, kStateOnly ? p.y : p.out};
     for (int i = 0; i < 4; ++i)
         if (!make_map(&m[i], ptr[i], B, p.geom, D)) return cudaErrorInvalidValue;
-    const long long items = p.geom.slots(p.seg) * p.geom.H;
-    const unsigned grid = (unsigned)(items < sms ? items : sms);
-    la_chunked_kernel<D, kRev, kStateOnly><<<grid, kThreads, Cfg<D>::kBytes, stream>>>(m[0], m[1], m[2],
+    const bool runs = !kStateOnly && p.run > 0;
+    const long long items = p.geom.slots(runs ? kChunk : p.seg) * p.geom.H;
+    const unsigned grid = (unsigned)(runs          ? (items + p.run - 1) / p.run
+                                     : items < sms ? items
+                                                   : sms);
+    la_chunked_kernel<D, kRev, kStateOnly, kGrad><<<grid, kThreads, Cfg<D>::kBytes, stream>>>(m[0], m[1], m[2],
                                                                                  m[3], p);
     return cudaGetLastError();
 }
 template <bool kRev, bool kStateOnly>
 inline cudaError_t launch_pass(const Pass<__nv_bfloat16>& p, int B, int D, cudaStream_t stream) {
-    return D == 64 ? launch_d<64, kRev, kStateOnly>(p, B, stream)
-                   : launch_d<128, kRev, kStateOnly>(p, B, stream);
+    if constexpr (!kStateOnly) {
+        if (p.dots)
+            return D == 64 ? launch_d<64, kRev, false, true>(p, B, stream)
+                           : launch_d<128, kRev, false, true>(p, B, stream);
+    }
+    return D == 64 ? launch_d<64, kRev, kStateOnly, false>(p, B, stream)
+                   : launch_d<128, kRev, kStateOnly, false>(p, B, stream);
 }
 
 }  // namespace tc

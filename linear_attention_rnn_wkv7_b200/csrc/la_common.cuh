@@ -140,6 +140,9 @@ struct Pass {
     float key_scale;      // on y_t z_t^T inside the state
     int parts;            // bf16 parts of the state update's operand (tensor cores): 3 where the
                           // state itself is a result, 1 where it only makes bf16 results
+    int run;              // > 0: chunks per block, see Schedule (tensor-core kernel); else segments
+    float* ho_state;      // [block][D * D], and
+    unsigned* ho_flag;    // [block][8], zero: states handed from block to block
     int seg;              // tokens per segment (a multiple of kChunk)
     const float* init;    // states before the first token: [N][H][D][D], or by slot when
     int init_by_slot;     // init_by_slot; nullptr: zeros
@@ -179,23 +182,30 @@ la_chain_kernel(Geom g, const float* __restrict__ init, float* __restrict__ seg_
     float4 S = make_float4(0.f, 0.f, 0.f, 0.f);
     if (init) S = reinterpret_cast<const float4*>(init)[i];
     const long long base = slot_of(g, it, 0, seg);
-    for (int jj = 0; jj < nseg; ++jj) {
-        const int j = kRev ? nseg - 1 - jj : jj;
-        const long long at = (base + j) * g.H + h;
-        float4* p = reinterpret_cast<float4*>(seg_state) + at * per + e;
-        const bool last = jj == nseg - 1;
-        float4 loc;
-        float d = 0.f;
-        if (!last) {
-            loc = *p;
-            d = seg_decay[at];
+    // four segments' own states in flight at a time
+    for (int j0 = 0; j0 < nseg; j0 += 4) {
+        float4 loc[4];
+        float d[4];
+        float4* at[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            const int jj = j0 + u, j = kRev ? nseg - 1 - jj : jj;
+            const long long slot = (base + j) * g.H + h;
+            at[u] = reinterpret_cast<float4*>(seg_state) + slot * per + e;
+            if (jj < nseg - 1) {  // (nothing starts from the last one's)
+                loc[u] = *at[u];
+                d[u] = seg_decay[slot];
+            }
         }
-        *p = S;
-        if (!last) {
-            S.x = fmaf(d, S.x, loc.x);
-            S.y = fmaf(d, S.y, loc.y);
-            S.z = fmaf(d, S.z, loc.z);
-            S.w = fmaf(d, S.w, loc.w);
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            if (j0 + u >= nseg) break;
+            *at[u] = S;
+            if (j0 + u == nseg - 1) break;
+            S.x = fmaf(d[u], S.x, loc[u].x);
+            S.y = fmaf(d[u], S.y, loc[u].y);
+            S.z = fmaf(d[u], S.z, loc[u].z);
+            S.w = fmaf(d[u], S.w, loc[u].w);
         }
     }
 }

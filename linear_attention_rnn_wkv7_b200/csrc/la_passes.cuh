@@ -23,40 +23,52 @@ struct Problem {
     int ends() const { return chunked ? D / 16 : D / 64; }
 };
 
-// Segments.  One segment per sequence needs nothing extra.  With fewer (sequence, head)
-// units than the GPU holds blocks, sequences are cut: a pass over y and z first gives every
-// segment's own state (half of a pass's reads, no outputs), la_chain_kernel joins them, and
-// all segments run at once.  The estimate below counts chunks on the longest block; the
-// extra launches and the join are charged as about three chunks.
+// How the work is laid out on the GPU.  One segment per sequence needs nothing extra.  With fewer
+// (sequence, head) units than the GPU holds blocks, sequences are cut: a pass over y and z first
+// gives every segment's own state (half of a pass's reads, no outputs), la_chain_kernel
+// joins them, and all segments run at once.  The estimate counts chunks of time on the longest
+// block: a segment costs about two more than its chunks (its state's way in and out), a state-only pass
+// 0.6 of a full one, the join a third per segment, the launches four.  With at least as many
+// units as blocks the tensor-core kernel takes runs (la_chunked.cuh, Schedule) instead.
 struct Plan {
     int seg;
     bool split;
+    int run;           // > 0: chunks per block
+    long long blocks;  // of the runs
 };
+constexpr int kBlocks = 148;  // SMs
+
 inline Plan make_plan(const Problem& p) {
     const Geom& g = p.geom;
     // blocks that run at once: one per SM (tensor cores) or by registers (64 a state tile)
-    const long long resident = p.chunked ? 148 : 148LL * 384 / p.D;
+    const long long resident = p.chunked ? kBlocks : (long long)kBlocks * 384 / p.D;
     const long long chunks = std::max<long long>(1, ((long long)g.T + kChunk - 1) / kChunk);
-    Plan best{(int)(chunks * kChunk), false};
+    Plan best{(int)(chunks * kChunk), false, 0, 0};
     if ((long long)chunks * kChunk > 0x7fffff80LL) best.seg = 0x7fffff80;
+    const long long units = (long long)g.N * g.H * p.slabs();
+    const long long all = g.slots(kChunk) * g.H;
+    if (p.chunked && units > kBlocks && all <= 0x7fffffffLL) {
+        const long long even = (all + kBlocks - 1) / kBlocks;
+        best.run = (int)(g.cu ? even : std::max(chunks, even));
+        best.blocks = (all + best.run - 1) / best.run;
+        return best;
+    }
     if (chunks < 4) return best;
     if (g.cu) {
         // lengths are on the device: cut only sequences longer than an even share
         const long long share = chunks * g.H * p.slabs() / resident;
         const long long c = std::max<long long>(4, share);
-        if (c < chunks) best = Plan{(int)(c * kChunk), true};
+        if (c < chunks) best = Plan{(int)(c * kChunk), true, 0, 0};
         return best;
     }
-    const long long units = (long long)g.N * g.H * p.slabs();
-    // (cut only for a gain beyond the estimate's own error)
-    double least = 0.85 * (double)((units + resident - 1) / resident) * (double)chunks;
+    double least = (double)((units + resident - 1) / resident) * (double)(chunks + 2);
     for (long long n = 2; n <= std::min<long long>(chunks, 256); ++n) {
         const long long c = (chunks + n - 1) / n, used = (chunks + c - 1) / c;
-        const long long waves = (units * used + resident - 1) / resident;
-        const double t = (double)(waves * c) * (1.0 + 0.5 * (double)(used - 1) / (double)used) + 3.0;
+        const double waves = (double)((units * used + resident - 1) / resident);
+        const double t = waves * (double)(c + 2) + waves * (0.6 * (double)c + 2) + 0.35 * (double)used + 4;
         if (used > 1 && t < least) {
             least = t;
-            best = Plan{(int)(c * kChunk), true};
+            best = Plan{(int)(c * kChunk), true, 0, 0};
         }
     }
     return best;
@@ -82,8 +94,27 @@ inline Segs carve_segs(Carve& c, const Problem& p, const Plan& plan) {
     s.decay = c.take(n * sizeof(float));
     return s;
 }
+// States handed from block to block, and their flags for `passes` passes.
+struct Handoff {
+    size_t state = 0, flags = 0, flag_bytes = 0;
+};
+inline Handoff carve_handoff(Carve& c, const Problem& p, const Plan& plan, int passes) {
+    Handoff h;
+    if (plan.run == 0) return h;
+    h.state = c.take((size_t)plan.blocks * p.D * p.D * sizeof(float));
+    h.flag_bytes = (size_t)passes * plan.blocks * 8 * sizeof(unsigned);
+    h.flags = c.take(h.flag_bytes);
+    return h;
+}
+template <typename Tin>
+inline void use_handoff(Pass<Tin>& a, const Plan& plan, const Handoff& h, uint8_t* ws, int pass) {
+    a.run = plan.run;
+    a.ho_state = reinterpret_cast<float*>(ws + h.state);
+    a.ho_flag = reinterpret_cast<unsigned*>(ws + h.flags) + (size_t)pass * plan.blocks * 8;
+}
 struct BwdSpace {
     Segs fwd, rev;
+    Handoff ho;
     size_t qdq, kdk, ck, ends, part, bytes;
 };
 inline BwdSpace carve_bwd(const Problem& p, const Plan& plan) {
@@ -91,6 +122,7 @@ inline BwdSpace carve_bwd(const Problem& p, const Plan& plan) {
     BwdSpace b;
     b.fwd = carve_segs(c, p, plan);
     b.rev = carve_segs(c, p, plan);
+    b.ho = carve_handoff(c, p, plan, 3);
     const size_t dots = (size_t)p.rows() * p.slabs() * sizeof(float);
     const size_t units = (size_t)p.geom.slots(p.ck_every()) * p.geom.H;
     b.qdq = c.take(dots);
@@ -103,7 +135,9 @@ inline BwdSpace carve_bwd(const Problem& p, const Plan& plan) {
 }
 inline size_t fwd_workspace(const Problem& p) {
     Carve c;
-    (void)carve_segs(c, p, make_plan(p));
+    const Plan plan = make_plan(p);
+    (void)carve_segs(c, p, plan);
+    (void)carve_handoff(c, p, plan, 1);
     return c.at;
 }
 inline size_t bwd_workspace(const Problem& p) { return carve_bwd(p, make_plan(p)).bytes; }
@@ -139,6 +173,7 @@ inline cudaError_t forward(const Problem& p, const Tin* q, const Tin* k, const T
     const Plan plan = make_plan(p);
     Carve c;
     const Segs s = carve_segs(c, p, plan);
+    const Handoff ho = carve_handoff(c, p, plan, 1);
     Pass<Tin> a{};
     a.geom = p.geom;
     a.x = q;
@@ -154,6 +189,12 @@ inline cudaError_t forward(const Problem& p, const Tin* q, const Tin* k, const T
     a.seg = plan.seg;
     a.init = s0;
     a.fin = sT;
+    if (plan.run > 0 && p.geom.T > 0) {
+        if (const cudaError_t e = cudaMemsetAsync(ws + ho.flags, 0, ho.flag_bytes, stream);
+            e != cudaSuccess)
+            return e;
+        use_handoff(a, plan, ho, ws, 0);
+    }
     if (plan.split) {
         if (const cudaError_t e = run_segments<Tin, false>(a, p, s0, ws, s, stream);
             e != cudaSuccess)
@@ -203,6 +244,13 @@ inline cudaError_t backward(const Problem& p, const Tin* q, const Tin* k, const 
         r.init = reinterpret_cast<float*>(ws + b.rev.state);
         f.init_by_slot = r.init_by_slot = 1;
     }
+    const bool runs = plan.run > 0 && p.geom.T > 0;
+    if (runs) {
+        const cudaError_t e = cudaMemsetAsync(ws + b.ho.flags, 0, b.ho.flag_bytes, stream);
+        if (e != cudaSuccess) return e;
+        use_handoff(f, plan, b.ho, ws, 0);
+        use_handoff(r, plan, b.ho, ws, 1);
+    }
     f.x = dout;
     f.y = v;
     f.z = k;
@@ -224,6 +272,7 @@ inline cudaError_t backward(const Problem& p, const Tin* q, const Tin* k, const 
     a.fin = ds0;
     if (e = run_pass<Tin, true, false>(a, p, stream); e != cudaSuccess) return e;
     a = r;  // dk = A'(v, do, q), state G^T
+    if (runs) use_handoff(a, plan, b.ho, ws, 2);
     a.x = v;
     a.y = dout;
     a.z = q;

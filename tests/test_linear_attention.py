@@ -192,7 +192,8 @@ def test_step_refuses(clib, kw, status):
 
 def test_workspace_queries(clib):
     q = lib.wkv7_la_workspace_bytes
-    assert q(8, 4096, 64) == 0                     # units enough: nothing is cut
+    assert q(8, 4096, 64, dtype=F32) == 0          # units enough: nothing is cut
+    assert q(8, 4096, 64) > 0                      # states handed from block to block
     assert q(1, 16384, 4) > 0 and q(1, 16384, 4, 128, 128) > q(1, 16384, 4)
     assert q(1, 100, 1) == 0 and q(1, 0, 1) == 0
     assert q(2, 100, 4, backward=True) > 0
@@ -264,6 +265,49 @@ def test_fwd_cut_into_segments(cuda_device, dtype, D, gate):
     compare_fwd(x, dtype, D, mask=True)
     x = make(1, 1500, 2, D, dtype, 12, gate, N=3)
     compare_fwd(x, dtype, D, cu=[0, 3, 1200, 1500])
+
+
+def many_sequences(D, seed, packed, head_first=False):
+    """More (sequence, head) pairs than SMs, so that sequences are cut between blocks: of one
+    length, or packed with lengths from 0 to more than a block's share."""
+    if not packed:
+        return make(40, 300, 4, D, BF16, seed, head_first=head_first), None
+    gen = torch.Generator().manual_seed(seed)
+    lens = [0, 1, 128, 700, 0] + torch.randint(0, 60, (45,), generator=gen).tolist() + [257, 0]
+    cu = [0]
+    for n in lens:
+        cu.append(cu[-1] + n)
+    return make(1, cu[-1], 4, D, BF16, seed, head_first=head_first, N=len(lens)), cu
+
+
+@gpu
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("packed,head_first", [(False, False), (True, False), (True, True)])
+def test_many_sequences(cuda_device, D, packed, head_first):
+    x, cu = many_sequences(D, 71, packed, head_first)
+    compare_fwd(x, BF16, D, cu=cu, head_first=head_first)
+    compare_bwd(x, BF16, D, cu=cu, head_first=head_first, mask=True)
+
+
+@gpu
+def test_many_sequences_repeat_and_replay(cuda_device):
+    """States handed between blocks: the same bits from call to call and from a replayed graph."""
+    x, cu = many_sequences(64, 73, True)
+    cu = torch.tensor(cu, dtype=torch.int32, device="cuda")
+    call = lambda: (lib.wkv7_la_fwd(x["q"], x["k"], x["v"], x["g"], s0=x["s0"], cu_seqlens=cu),  # noqa: E731
+                    lib.wkv7_la_bwd(x["q"], x["k"], x["v"], x["g"], x["do"], cu_seqlens=cu))
+    (o, s), b = call()
+    graph = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        (o2, s2), b2 = call()
+    for _ in range(3):
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(o, o2) and torch.equal(s, s2)
+        for n in b:
+            assert torch.equal(b[n], b2[n]), n
+    assert lib.wkv7_get_last_error() == OK
 
 
 @gpu
