@@ -74,8 +74,12 @@ struct Cfg {
     static constexpr int OFF_PARTS = OFF_STATE + kStateBytes;
     static constexpr int OFF_SC = OFF_PARTS + (kPartsInPlace ? 0 : 4 * kTile);
     static constexpr int kScBytes = 2 * 512 + 64;     // struct Scan
-    static constexpr int OFF_BAR = OFF_SC + kStages * kScBytes;
-    static constexpr int kBytes = OFF_BAR + 256;
+    // Slots of decays: with two for each stage, a slot is used again only when a chunk that
+    // came after all its readers' work is done (one for each stage where there is no room:
+    // free with the stage's Z, behind the output).
+    static constexpr int kScans = kAhead ? 2 * kStages : kStages;
+    static constexpr int OFF_BAR = OFF_SC + kScans * kScBytes;
+    static constexpr int kBytes = OFF_BAR + 352;
     // tensor memory columns
     static constexpr int TM_P = 0, TM_OI = kAhead ? 256 : 128, TM_OX = TM_OI + D, TM_DU = TM_OX + D;
 };
@@ -191,20 +195,22 @@ __device__ __forceinline__ void umma_bf16_ts(uint32_t tmem_d, uint32_t tmem_a, u
 
 // The CTA's barriers (8 bytes each, from OFF_BAR).
 enum Bar {
-    kFull = 0,     // [4] a stage's tiles have landed
-    kEmpty = 4,    // [4] a stage may be loaded again
-    kScan = 8,     // [4] a stage's decays are there (and its unused Z rows are clear)
-    kStore = 12,   // [4] a stage's output tile is in shared memory
-    kScore = 16,   // [2] P = X Y^T is done
-    kCross = 18,   // [2] Ox = X U0 is done
-    kPReady = 20,  // [2] P in bf16 is in tensor memory
-    kKReady = 22,  // [2] k . Y is in shared memory
-    kDelta = 24,   // [2] dU is done
-    kSReady = 26,  // U0 in bf16 is in shared memory (and the last dU has been read)
-    kOut = 27,     // Ox, Oi and every other product of the chunk are done
-    kOFree = 28,   // Ox and Oi have been read
-    kDrain = 29,   // after an abort: all MMAs are done
-    kBars = 30
+    kFull = 0,     // [4] a stage's X and Y have landed
+    kFullZ = 4,    // [4] a stage's Z has landed
+    kEmpty = 8,    // [4] a stage's X and Y may be loaded again
+    kEmptyZ = 12,  // [4] a stage's Z may be loaded again
+    kScan = 16,    // [6] a chunk's decays are there (and its unused Z rows are clear)
+    kScore = 22,   // [2] P = X Y^T is done
+    kCross = 24,   // [2] Ox = X U0 is done
+    kPReady = 26,  // [2] P in bf16 is in tensor memory
+    kKReady = 28,  // [2] k . Y is in shared memory
+    kDelta = 30,   // [2] dU is done
+    kStore = 32,   // [4] a stage's output tile is in shared memory
+    kSReady = 36,  // U0 in bf16 is in shared memory (and the last dU has been read)
+    kOut = 37,     // Ox, Oi and every other product of the chunk are done
+    kOFree = 38,   // Ox and Oi have been read
+    kDrain = 39,   // after an abort: all MMAs are done
+    kBars = 40
 };
 
 // The slow path of a wait, kept out of line (the roles' code has to fit the instruction
@@ -259,16 +265,21 @@ struct Ctx {
     }
 };
 
-// A role's place in the list of chunks: the n-th of the CTA, in stage st for the ph-th time.
-template <int NS>
+// A role's place in the list of chunks: the n-th of the CTA, in stage st for the ph-th time and
+// in decay slot sc for the sp-th.
+template <int NS, int NC>
 struct Place {
-    int n = 0, st = 0;
-    uint32_t ph = 0;
+    int n = 0, st = 0, sc = 0;
+    uint32_t ph = 0, sp = 0;
     __device__ __forceinline__ void next() {
         ++n;
         if (++st == NS) {
             st = 0;
             ph ^= 1;
+        }
+        if (++sc == NC) {
+            sc = 0;
+            sp ^= 1;
         }
     }
     __device__ __forceinline__ uint32_t odd() const { return n & 1; }          // one barrier
@@ -476,7 +487,7 @@ la_chunked_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constan
     if (tid == 32) {
         *cx.abort = 0;
         for (int i = 0; i < kBars; ++i) {
-            const int count = i >= kEmpty && i < kEmpty + 4 ? (kStateOnly ? 32 * C::kStateWarps : 1)
+            const int count = i >= kEmptyZ && i < kEmptyZ + 4 ? (kStateOnly ? 32 * C::kStateWarps : 1)
                               : i >= kStore && i < kStore + 4 ? 128
                               : i == kPReady || i == kPReady + 1 || i == kOFree ? 128
                               : i == kKReady || i == kKReady + 1 ? 256
@@ -491,18 +502,22 @@ la_chunked_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constan
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
 
-    auto scan_of = [&](int st) {
-        return reinterpret_cast<Scan*>(smem + C::OFF_SC + st * C::kScBytes);
+    auto scan_of = [&](int sc) {
+        return reinterpret_cast<Scan*>(smem + C::OFF_SC + sc * C::kScBytes);
     };
     Walk<kRev, kStateOnly> wk(p);
-    Place<NS> at_;
+    using Spot = Place<NS, C::kScans>;
+    Spot at_;
     int& n = at_.n;
 
+    // A chunk's output is staged over its Z once all its products are done (Z is the tile that
+    // the next chunk of the stage needs last; X and Y are loaded again before).
+    auto out_tile = [&](const Spot& at) { return cx.sbase + at.st * C::kStage + 2 * C::kTile; };
     // k . Y of one chunk, in bf16 parts: the first over Y itself.  Two groups of four warps take
     // half of it each: of the rows at D = 64, of the columns at D = 128.
-    auto scale_keys = [&](const Place<NS>& at, int half) {
+    auto scale_keys = [&](const Spot& at, int half) {
         const int st = at.st;
-        if (!cx.wait_warp(kScan + st, at.ph)) return false;
+        if (!cx.wait_warp(kScan + at.sc, at.sp)) return false;
         if (!cx.wait_warp(kFull + st, at.ph)) return false;
         if (!kStateOnly && !cx.wait_warp(kScore + (at.n & 1), at.pair())) return false;
         if (C::kPartsInPlace) {
@@ -517,7 +532,7 @@ la_chunked_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constan
             C::kPartsInPlace ? x : cx.sbase + C::OFF_PARTS + 2 * C::kTile * (at.n & 1);
         const uint32_t part2 = C::kPartsInPlace ? cx.sbase + C::OFF_STATE : part1 + C::kTile;
         const uint32_t o = D == 64 ? 0 : half * C::kSub;
-        split_keys(y + o, part1 + o, part2 + o, scan_of(st), D == 64 ? half * 512 : 0, D / 16,
+        split_keys(y + o, part1 + o, part2 + o, scan_of(at.sc), D == 64 ? half * 512 : 0, D / 16,
                    p.parts);
         fence_proxy_async();
         cx.arrive(kKReady + (at.n & 1));
@@ -528,26 +543,37 @@ la_chunked_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constan
     if (warp == 0) {
         if (lane == 0) {
             bool ok = true;
+            int z_loads = 0;
             while (ok && wk.next(p)) {
                 for (int i = 0; ok && i < wk.chunks; ++i, at_.next()) {
                     const int st = at_.st;
                     if (n >= NS && !(ok = cx.wait(kEmpty + st, at_.ph ^ 1))) break;
                     const uint32_t full = cx.bar(kFull + st), at = cx.sbase + st * C::kStage;
-                    mbar_arrive_expect_tx(full, (kStateOnly ? 2 : 3) * C::kTile);
+                    const uint32_t fz = cx.bar(kFullZ + st);
+                    mbar_arrive_expect_tx(full, (kStateOnly ? 1 : 2) * C::kTile);
                     const At a = tma_row(G, wk.it, wk.h, wk.first_token(i));
 #pragma unroll
                     for (int s = 0; s < D / 64; ++s) {
                         if (!kStateOnly)
                             tma_load_3d(at + s * C::kSub, &tm_x, full, 64 * s, a.c1, a.c2);
                         tma_load_3d(at + C::kTile + s * C::kSub, &tm_y, full, 64 * s, a.c1, a.c2);
-                        tma_load_3d(at + 2 * C::kTile + s * C::kSub, &tm_z, full, 64 * s, a.c1,
-                                    a.c2);
                     }
+                    if (n >= NS && !(ok = cx.wait(kEmptyZ + st, at_.ph ^ 1))) {
+                        at_.next();  // (for the drain below)
+                        break;
+                    }
+                    mbar_arrive_expect_tx(fz, C::kTile);
+#pragma unroll
+                    for (int s = 0; s < D / 64; ++s)
+                        tma_load_3d(at + 2 * C::kTile + s * C::kSub, &tm_z, fz, 64 * s, a.c1, a.c2);
+                    z_loads = n + 1;
                 }
             }
             if (!ok) {  // the copies in flight land before the CTA leaves (bounded)
                 for (int m = n < NS ? 0 : n - NS; m < n; ++m)
                     (void)mbar_wait(cx.bar(kFull + m % NS), (m / NS) & 1);
+                for (int m = z_loads < NS ? 0 : z_loads - NS; m < z_loads; ++m)
+                    (void)mbar_wait(cx.bar(kFullZ + m % NS), (m / NS) & 1);
             }
         }
     }
@@ -566,7 +592,7 @@ la_chunked_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constan
             const uint64_t kmaj = smem_desc(0, 16, 1024);                  // K-major
             const uint64_t mn_tile = smem_desc(0, C::kSub, 1024);          // MN-major tiles
             const uint64_t mn_state = smem_desc(0, C::kStateSub, 1024);    // MN-major U0
-            Place<NS> sc_at;
+            Spot sc_at;
             auto score = [&]() {  // P = X Y^T of the next chunk
                 const int st = sc_at.st, m = sc_at.n;
                 if (!cx.wait_warp(kFull + st, sc_at.ph)) return false;
@@ -590,6 +616,7 @@ la_chunked_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constan
                 const uint32_t x = (cx.sbase + st * C::kStage) >> 4, y = x + (C::kTile >> 4),
                                z = y + (C::kTile >> 4), state = (cx.sbase + C::OFF_STATE) >> 4;
                 auto delta = [&]() {  // dU, from the parts of k . Y
+                    if (!cx.wait_warp(kFullZ + st, at_.ph)) return false;
                     if (!cx.wait_warp(kKReady + (n & 1), at_.pair())) return false;
                     tc_fence_after();
                     const uint32_t own =
@@ -630,7 +657,8 @@ la_chunked_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constan
                     }
                     if (leader) umma_commit(cx.bar(kCross + (n & 1)));
                     if (!cx.wait_warp(kPReady + (n & 1), at_.pair())) return false;
-                    if (!cx.wait_warp(kScan + st, at_.ph)) return false;  // Z's rows are clear
+                    if (!cx.wait_warp(kScan + at_.sc, at_.sp)) return false;  // Z's rows are clear
+                    if (!cx.wait_warp(kFullZ + st, at_.ph)) return false;
                     tc_fence_after();
                     b = mn_tile + z;
                     const uint32_t tp = tmem + C::TM_P + (C::kAhead ? 128 * (n & 1) : 0);
@@ -640,7 +668,10 @@ la_chunked_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constan
                     if (!C::kAhead && more && !score()) return false;
                 }
                 if ((!C::kAhead || kStateOnly) && !delta()) return false;
-                if (leader) umma_commit(cx.bar(kOut));
+                if (leader) {  // the chunk's tiles have been read, too
+                    umma_commit(cx.bar(kOut));
+                    umma_commit(cx.bar(kEmpty + st));
+                }
                 return true;
             };
             // chunks left in this and later segments decide whether another score follows
@@ -744,8 +775,10 @@ la_chunked_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constan
                     if (!kRev) d += gl[q];
                 }
                 const float tail = __shfl_sync(0xffffffffu, gl[0], lane & 24);  // rev: the border's own
-                if (n >= NS && !(ok = cx.wait_warp(kEmpty + st, at_.ph ^ 1))) break;
-                Scan* sc = scan_of(st);
+                if (n >= NS &&
+                    !(ok = cx.wait_warp((C::kAhead ? kEmpty : kEmptyZ) + st, at_.ph ^ 1)))
+                    break;
+                Scan* sc = scan_of(at_.sc);
                 *reinterpret_cast<float4*>(&sc->c[4 * lane]) = make_float4(cc[0], cc[1], cc[2], cc[3]);
                 *reinterpret_cast<float4*>(&sc->f[4 * lane]) = make_float4(ff[0], ff[1], ff[2], ff[3]);
                 // 8 lanes make a 32-token word
@@ -767,7 +800,7 @@ la_chunked_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constan
                 }
                 // rows of Z that do not enter may hold anything (0 * NaN is NaN): clear them
                 if (__any_sync(0xffffffffu, enter != 15u)) {
-                    if (!(ok = cx.wait_warp(kFull + st, at_.ph))) break;
+                    if (!(ok = cx.wait_warp(kFullZ + st, at_.ph))) break;
                     const uint32_t z = cx.sbase + st * C::kStage + 2 * C::kTile;
                     for (int q = 0; q < 4; ++q) {
                         if ((enter >> q) & 1) continue;
@@ -778,7 +811,7 @@ la_chunked_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constan
                     fence_proxy_async();
                 }
                 __syncwarp();
-                if (lane == 0) cx.arrive(kScan + st);
+                if (lane == 0) cx.arrive(kScan + at_.sc);
             }
         }
     }
@@ -789,9 +822,9 @@ la_chunked_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constan
             while (ok && wk.next(p)) {
                 const Rows rw = rows_of(G, wk.it, wk.h);
                 for (int i = 0; ok && i < wk.chunks; ++i, at_.next()) {
-                    const int st = at_.st, t0 = wk.first_token(i);
-                    if (!(ok = cx.wait_warp(kStore + st, at_.ph))) break;
-                    const uint32_t tile = cx.sbase + st * C::kStage + 2 * C::kTile;
+                    const int t0 = wk.first_token(i);
+                    if (!(ok = cx.wait_warp(kStore + at_.st, at_.ph))) break;
+                    const uint32_t tile = out_tile(at_);
                     if (t0 + kChunk <= wk.te) {
                         if (lane == 0) {
                             const At a = tma_row(G, wk.it, wk.h, t0);
@@ -812,7 +845,7 @@ la_chunked_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constan
                         fence_proxy_async();  // the stage's next copy comes behind these reads
                     }
                     __syncwarp();
-                    if (lane == 0) cx.arrive(kEmpty + st);
+                    if (lane == 0) cx.arrive(kEmptyZ + at_.st);
                 }
             }
             if (lane == 0) bulk_wait0();
@@ -831,8 +864,8 @@ la_chunked_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constan
                 }
                 const uint32_t tp = tmem + ((uint32_t)(32 * w) << 16) + C::TM_P +
                                     (C::kAhead ? 128 * (n & 1) : 0);
-                if (!(ok = cx.wait_warp(kScan + st, at_.ph))) break;
-                const Scan* sc = scan_of(st);
+                if (!(ok = cx.wait_warp(kScan + at_.sc, at_.sp))) break;
+                const Scan* sc = scan_of(at_.sc);
                 const float ct = sc->c[row];
                 if (!(ok = cx.wait_warp(kScore + (n & 1), at_.pair()))) break;
                 tc_fence_after();
@@ -968,7 +1001,7 @@ la_chunked_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constan
             tc_fence_before();
             cx.arrive(kSReady);
         };
-        Place<NS> keys;
+        Spot keys;
         float decay = 0.f, next_decay = 0.f;
         int more = 0, next_more = 0;
         while (ok && wk.next(p)) {
@@ -995,18 +1028,17 @@ la_chunked_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constan
             }
             float logs = 0.f;
             for (int i = 0; ok && i < wk.chunks; ++i, at_.next()) {
-                const int st = at_.st, t0 = wk.first_token(i);
-                const uint32_t z = cx.sbase + st * C::kStage + 2 * C::kTile;
+                const int t0 = wk.first_token(i);
                 // What the state's warps need of a stage's decays they read before they give
                 // that chunk's U0: from then on the stage may be used up and refilled.
                 if (!C::kAhead || n == 0) {
-                    if (!(ok = cx.wait_warp(kScan + st, at_.ph))) break;
-                    decay = scan_of(st)->decay;
-                    more = scan_of(st)->more;
+                    if (!(ok = cx.wait_warp(kScan + at_.sc, at_.sp))) break;
+                    decay = scan_of(at_.sc)->decay;
+                    more = scan_of(at_.sc)->more;
                 }
                 if (has_state && (C::kAhead || i == 0)) publish_state();
-                const Scan* sc = scan_of(st);
-                if (kStateOnly) logs += sc->c[127];
+                const Scan* sc = scan_of(at_.sc);
+                if (kStateOnly && has_state) logs += sc->c[127];
                 float rowf = 0.f;
                 bool row_out = true;
                 if (!kStateOnly && !first) {
@@ -1019,8 +1051,8 @@ la_chunked_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constan
                 if (C::kAhead) {
                     for (int k = n == 0 ? 0 : 1; ok && k < 1 + (more ? 1 : 0); ++k) {
                         ok = scale_keys(keys, first ? 0 : 1);
-                        next_decay = scan_of(keys.st)->decay;
-                        next_more = scan_of(keys.st)->more;
+                        next_decay = scan_of(keys.sc)->decay;
+                        next_more = scan_of(keys.sc)->more;
                         keys.next();
                     }
                 } else if (first) {
@@ -1089,7 +1121,7 @@ la_chunked_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constan
                         !(ok = cx.wait_warp(kCross + (n & 1), at_.pair())))
                         break;
                     if (!C::kAhead && i + 1 < wk.chunks) publish_state();  // (before any output)
-                    if (kStateOnly) cx.arrive(kEmpty + st);
+                    if (kStateOnly) cx.arrive(kEmptyZ + at_.st);
                 }
                 if (C::kAhead) {
                     decay = next_decay;
@@ -1099,6 +1131,7 @@ la_chunked_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constan
                 if (!kStateOnly && !first) {  // outputs
                     if (!(ok = cx.wait_warp(kOut, at_.odd()))) break;
                     tc_fence_after();
+                    const uint32_t tile = out_tile(at_);
                     const int row = 32 * w + lane, t = t0 + row;
                     const bool in = t < wk.te;
                     const long long grow = rw.first + (long long)t * rw.step;
@@ -1142,7 +1175,7 @@ la_chunked_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constan
                                 }
                             }
                         }
-                        const uint32_t base = z + (q / 64) * C::kSub + row * 128;
+                        const uint32_t base = tile + (q / 64) * C::kSub + row * 128;
 #pragma unroll
                         for (int u = 0; u < V / 8; ++u) {
                             uint32_t pk[4];
@@ -1157,7 +1190,7 @@ la_chunked_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constan
                     cx.arrive(kOFree);
                     if (kGrad && in) p.dots[grow] = dot;
                     fence_proxy_async();
-                    cx.arrive(kStore + st);
+                    cx.arrive(kStore + at_.st);
                 }
             }
             if (!ok) break;
