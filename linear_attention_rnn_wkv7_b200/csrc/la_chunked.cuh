@@ -113,9 +113,6 @@ __device__ __forceinline__ void st_shared16(uint32_t addr, uint32_t a, uint32_t 
                  "r"(d)
                  : "memory");
 }
-__device__ __forceinline__ void st_shared4(uint32_t addr, uint32_t a) {
-    asm volatile("st.shared.b32 [%0], %1;" ::"r"(addr), "r"(a) : "memory");
-}
 __device__ __forceinline__ uint4 ld_shared16(uint32_t addr) {
     uint4 v;
     asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
@@ -151,31 +148,19 @@ __device__ __forceinline__ uint32_t pack2(uint64_t x) {
 __device__ __forceinline__ uint64_t unpack2(uint32_t x) {
     return pair2(__uint_as_float(x << 16), __uint_as_float(x & 0xffff0000u));
 }
-// 32 lanes x 32 columns: thread i gets lane i's.
-__device__ __forceinline__ void tmem_ld32(uint32_t taddr, float (&v)[32]) {
-    uint32_t r[32];
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, "
-        "%11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, "
-        "%28, %29, %30, %31}, [%32];"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
-          "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]),
-          "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]),
-          "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
-          "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]),
-          "=r"(r[31])
-        : "r"(taddr));
-#pragma unroll
-    for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
+// 32 lanes x 8 columns of packed bf16 pairs.
+__device__ __forceinline__ void tmem_st_raw8(uint32_t taddr, const uint32_t (&v)[8]) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(
+                     taddr),
+                 "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+                 : "memory");
 }
-// 32 lanes x 16 columns of packed bf16 pairs.
-__device__ __forceinline__ void tmem_st_raw16(uint32_t taddr, const uint32_t (&v)[16]) {
-    asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, "
-        "%11, %12, %13, %14, %15, %16};" ::"r"(taddr),
-        "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]),
-        "r"(v[8]), "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
-        : "memory");
+// Four 8 x 8 blocks of 16-bit pairs, a warp-MMA fragment each, to rows of 16 bytes: lane l gives the
+// address of row l % 8 of block l / 8.
+__device__ __forceinline__ void stmatrix4(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+    asm volatile("stmatrix.sync.aligned.m8n8.x4.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a),
+                 "r"(b), "r"(c), "r"(d)
+                 : "memory");
 }
 // One lane of a converged warp.
 __device__ __forceinline__ bool elect_one() {
@@ -213,8 +198,10 @@ enum Bar {
     kBars = 40
 };
 
-// The slow path of a wait, kept out of line (the roles' code has to fit the instruction
-// caches): polls for at most a second, or until another thread has given up.
+// The slow path of a wait, out of line: the roles' code has to fit the SM's instruction cache
+// together (as unrolled as each role alone would like it did not, and with all SMs at it
+// every role ran at the pace of instruction fetches from the level behind, half as fast).
+// Polls for at most a second, or until another thread has given up.
 __device__ __noinline__ bool wait_slow(uint32_t bar, uint32_t parity, volatile int* abort) {
     uint64_t t0 = 0;
     for (uint32_t k = 0; k < (1u << 28); ++k) {
@@ -304,85 +291,81 @@ struct Piece {
     int h, slot, tb, te, chunks;  // tokens [tb, te) of the sequence
     bool begins, ends;            // its first (last) chunk in the direction of the pass is the sequence's
 };
-// The segment of that number, if it has work (chunks >= 0).  Out of line: divisions, in
-// every role.
-__device__ __noinline__ Piece find_segment(const Geom& g, int seg, int item, int rev, int state_only) {
+struct Cursor {
+    int item, items;  // segments; or positions: the next one, the run's first
+    int slots;        // of the chunks (runs), 0: segments
+};
+// The cursor's next piece; chunks < 0: none left.  Out of line: divisions, in every role.
+__device__ __noinline__ Piece next_piece(const Geom& g, int seg, Cursor& at, int rev, int state_only) {
     Piece s;
-    s.slot = item / g.H;
-    s.h = item - s.slot * g.H;
-    s.it = locate(g, s.slot, seg);
     s.tb = s.te = 0;
     s.chunks = -1;
-    if (s.it.n < 0) return s;
-    s.begins = rev ? s.it.j == s.it.nseg - 1 : s.it.j == 0;
-    s.ends = rev ? s.it.j == 0 : s.it.j == s.it.nseg - 1;
-    if (state_only && s.ends) return s;
-    s.tb = s.it.j * seg;
-    s.te = s.it.len - s.tb < seg ? s.it.len : s.tb + seg;
-    s.chunks = (s.te - s.tb + kChunk - 1) / kChunk;
-    return s;
-}
-// The piece that ends at position pos of a run that starts at `start`; `pos` becomes the position
-// before it.
-__device__ __noinline__ Piece find_piece(const Geom& g, int slots, int start, int& pos, int rev) {
-    Piece s;
-    s.h = pos / slots;
-    const int at = pos - s.h * slots;
-    s.slot = rev ? slots - 1 - at : at;
-    s.it = locate(g, s.slot, kChunk);
-    s.tb = s.te = 0;
-    s.chunks = -1;
-    if (s.it.n < 0) {
-        --pos;
+    s.begins = s.ends = false;
+    if (at.slots == 0) {
+        while (at.items - at.item > (int)gridDim.x) {
+            at.item += gridDim.x;
+            s.slot = at.item / g.H;
+            s.h = at.item - s.slot * g.H;
+            s.it = locate(g, s.slot, seg);
+            if (s.it.n < 0) continue;
+            s.begins = rev ? s.it.j == s.it.nseg - 1 : s.it.j == 0;
+            s.ends = rev ? s.it.j == 0 : s.it.j == s.it.nseg - 1;
+            if (state_only && s.ends) continue;  // (its state starts no other segment)
+            s.tb = s.it.j * seg;
+            s.te = s.it.len - s.tb < seg ? s.it.len : s.tb + seg;
+            s.chunks = (s.te - s.tb + kChunk - 1) / kChunk;
+            return s;
+        }
         return s;
     }
-    const int total = s.it.nseg;  // chunks [first, last] in the direction of the pass
-    const int last = rev ? total - 1 - s.it.j : s.it.j;
-    const int first = last - (pos - start) > 0 ? last - (pos - start) : 0;
-    s.begins = first == 0;
-    s.ends = last == total - 1;
-    s.tb = kChunk * (rev ? total - 1 - last : first);
-    const int te = kChunk * (rev ? total - first : last + 1);
-    s.te = s.it.len < te ? s.it.len : te;
-    s.chunks = (s.te - s.tb + kChunk - 1) / kChunk;
-    pos -= last - first + 1;
+    while (at.item >= at.items) {
+        const int pos = at.item;
+        s.h = pos / at.slots;
+        const int in_head = pos - s.h * at.slots;
+        s.slot = rev ? at.slots - 1 - in_head : in_head;
+        s.it = locate(g, s.slot, kChunk);
+        if (s.it.n < 0) {
+            --at.item;
+            continue;
+        }
+        const int total = s.it.nseg;  // chunks [first, last] in the direction of the pass
+        const int last = rev ? total - 1 - s.it.j : s.it.j;
+        const int first = last - (pos - at.items) > 0 ? last - (pos - at.items) : 0;
+        s.begins = first == 0;
+        s.ends = last == total - 1;
+        s.tb = kChunk * (rev ? total - 1 - last : first);
+        const int te = kChunk * (rev ? total - first : last + 1);
+        s.te = s.it.len < te ? s.it.len : te;
+        s.chunks = (s.te - s.tb + kChunk - 1) / kChunk;
+        at.item = pos - (last - first + 1);
+        return s;
+    }
     return s;
 }
 template <bool kRev, bool kStateOnly>
 struct Walk : Piece {
-    int item, items;   // segments; or positions: the next one, the run's first
-    int slots;
+    Cursor at;
     template <typename P>
     __device__ __forceinline__ explicit Walk(const P& p) {
         const Geom& g = p.geom;
         if (kStateOnly || p.run == 0) {
-            slots = 0;
-            item = (int)blockIdx.x - (int)gridDim.x;
-            items = (int)(g.slots(p.seg) * g.H);
+            at.slots = 0;
+            at.item = (int)blockIdx.x - (int)gridDim.x;
+            at.items = (int)(g.slots(p.seg) * g.H);
         } else {
-            slots = (int)g.slots(kChunk);
-            const long long all = (long long)slots * g.H, start = (long long)blockIdx.x * p.run;
-            items = (int)start;
-            item = (int)(start + p.run < all ? start + p.run : all) - 1;
+            at.slots = (int)g.slots(kChunk);
+            const long long all = (long long)at.slots * g.H, start = (long long)blockIdx.x * p.run;
+            at.items = (int)start;
+            at.item = (int)(start + p.run < all ? start + p.run : all) - 1;
         }
     }
     // The next piece; false: none left.
     template <typename P>
     __device__ __forceinline__ bool next(const P& p) {
-        if (kStateOnly || slots == 0) {
-            while (items - item > (int)gridDim.x) {
-                item += gridDim.x;
-                static_cast<Piece&>(*this) =
-                    find_segment(p.geom, p.seg, item, kRev, kStateOnly);
-                if (this->chunks >= 0) return true;
-            }
-        } else {
-            while (item >= items) {
-                static_cast<Piece&>(*this) = find_piece(p.geom, slots, items, item, kRev);
-                if (this->chunks >= 0) return true;
-            }
-        }
-        return false;
+        Cursor c = at;
+        static_cast<Piece&>(*this) = next_piece(p.geom, p.seg, c, kRev, kStateOnly);
+        at = c;
+        return this->chunks >= 0;
     }
     __device__ __forceinline__ int first_token(int i) const {
         return this->tb + kChunk * (kRev ? this->chunks - 1 - i : i);
@@ -611,7 +594,9 @@ la_chunked_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constan
                 if (leader) umma_commit(cx.bar(kScore + (m & 1)));
                 return true;
             };
-            auto chunk = [&](bool more) {  // the products of chunk n (more: another follows)
+            // The products of chunk n, and the score of the one after it (more); n = -1 for the
+            // first score alone.
+            auto chunk = [&](bool chunk_n, bool more) {
                 const int st = at_.st;
                 const uint32_t x = (cx.sbase + st * C::kStage) >> 4, y = x + (C::kTile >> 4),
                                z = y + (C::kTile >> 4), state = (cx.sbase + C::OFF_STATE) >> 4;
@@ -639,10 +624,11 @@ la_chunked_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constan
                 };
                 if (C::kAhead && !kStateOnly) {
                     if (more && !score()) return false;
+                    if (!chunk_n) return true;
                     if (!delta()) return false;  // (its last user's dU was read before U0 came)
                 }
-                if (!cx.wait_warp(kSReady, at_.odd())) return false;
-                if (!kStateOnly) {
+                if (chunk_n && !cx.wait_warp(kSReady, at_.odd())) return false;
+                if (!kStateOnly && chunk_n) {
                     if (n > 0 && !cx.wait_warp(kOFree, at_.odd() ^ 1)) return false;
                     tc_fence_after();
                     uint64_t a = kmaj + x, b = mn_state + state;
@@ -657,15 +643,19 @@ la_chunked_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constan
                     }
                     if (leader) umma_commit(cx.bar(kCross + (n & 1)));
                     if (!cx.wait_warp(kPReady + (n & 1), at_.pair())) return false;
-                    if (!cx.wait_warp(kScan + at_.sc, at_.sp)) return false;  // Z's rows are clear
-                    if (!cx.wait_warp(kFullZ + st, at_.ph)) return false;
+                    // Z, its unused rows clear (where dU is ahead it has waited for both)
+                    if (!C::kAhead && !cx.wait_warp(kScan + at_.sc, at_.sp)) return false;
+                    if (!C::kAhead && !cx.wait_warp(kFullZ + st, at_.ph)) return false;
                     tc_fence_after();
                     b = mn_tile + z;
                     const uint32_t tp = tmem + C::TM_P + (C::kAhead ? 128 * (n & 1) : 0);
 #pragma unroll
                     for (int kk = 0; kk < 8; ++kk)
                         if (leader) umma_bf16_ts(tmem + C::TM_OI, tp + 8 * kk, b + 128 * kk, id_out, kk > 0);
-                    if (!C::kAhead && more && !score()) return false;
+                }
+                if (!C::kAhead && !kStateOnly) {
+                    if (more && !score()) return false;
+                    if (!chunk_n) return true;
                 }
                 if ((!C::kAhead || kStateOnly) && !delta()) return false;
                 if (leader) {  // the chunk's tiles have been read, too
@@ -674,15 +664,20 @@ la_chunked_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constan
                 }
                 return true;
             };
-            // chunks left in this and later segments decide whether another score follows
-            bool have = wk.next(p);
-            while (have && wk.chunks == 0) have = wk.next(p);
-            if (have && !kStateOnly) ok = score();
-            while (ok && have) {
-                const int here = __shfl_sync(0xffffffffu, wk.chunks, 0);
-                have = wk.next(p);
+            // Chunk m's score goes with the products of chunk m - 1, so the list is walked one
+            // chunk ahead of the products.
+            bool started = kStateOnly;
+            while (ok) {
+                bool have = wk.next(p);
                 while (have && wk.chunks == 0) have = wk.next(p);
-                for (int i = 0; ok && i < here; ++i, at_.next()) ok = chunk(i + 1 < here || have);
+                const int here = have ? __shfl_sync(0xffffffffu, wk.chunks, 0) : (started && !kStateOnly ? 1 : 0);
+                if (here == 0) break;
+                for (int i = 0; ok && i < here; ++i) {
+                    ok = chunk(started, have);
+                    if (started) at_.next();
+                    started = true;
+                }
+                if (!have) break;
             }
             if (!ok) {
                 if (leader) umma_commit(cx.bar(kDrain));
@@ -771,7 +766,7 @@ la_chunked_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constan
                 for (int u = 0; u < 4; ++u) {
                     const int q = kRev ? u : 3 - u;
                     if (kRev && !((lane & 7) == 0 && q == 0)) d += gl[q];
-                    ff[q] = (enter >> q) & 1 ? expf(d) : 0.f;
+                    ff[q] = (enter >> q) & 1 ? ex2(d * kLog2e) : 0.f;
                     if (!kRev) d += gl[q];
                 }
                 const float tail = __shfl_sync(0xffffffffu, gl[0], lane & 24);  // rev: the border's own
@@ -791,7 +786,7 @@ la_chunked_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constan
                 if ((lane & 7) == 0) {
                     sc->live[blk] = lw;
                     sc->out[blk] = ow;
-                    sc->kb[blk] = p.key_scale * expf(kRev ? before + tail : after);
+                    sc->kb[blk] = p.key_scale * ex2(kLog2e * (kRev ? before + tail : after));
                 }
                 // (1 + the small difference: a constant decay's rounding repeats every chunk)
                 if (lane == 0) {
@@ -872,51 +867,53 @@ la_chunked_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constan
                 // Loops stay rolled: four roles share the instruction cache of each
                 // sub-partition, and one warp running long straight code is fetch-bound.
 #pragma unroll 1
-                for (int b = 0; b < 4; ++b) {
-                    uint32_t out[16];
-                    const uint32_t live = sc->live[b];
+                for (int hb = 0; hb < 8; ++hb) {  // 16 columns at a time
+                    const int b = hb >> 1, col = 16 * hb;
+                    uint32_t out[8];
                     if (kRev ? b < w : b > w) {
 #pragma unroll
-                        for (int q = 0; q < 16; ++q) out[q] = 0;
-                    } else if (b != w && live == 0xffffffffu) {
-                        // token to its block's border to this row: both exponents <= 0
-                        const float border = sc->c[kRev ? 32 * b : 32 * b + 31];
-                        const float r = p.pair_scale * ex2(kRev ? border - ct : ct - border);
-                        float v[32];
-                        tmem_ld32(tp + 32 * b, v);
-                        tmem_ld_wait();
-                        const uint64_t rr = pair2(r, r);
-#pragma unroll
-                        for (int q = 0; q < 32; q += 4) {
-                            const ulonglong2 f =
-                                *reinterpret_cast<const ulonglong2*>(&sc->f[32 * b + q]);
-                            out[q / 2] = pack2(mul2(mul2(pair2(v[q], v[q + 1]), rr), f.x));
-                            out[q / 2 + 1] = pack2(mul2(mul2(pair2(v[q + 2], v[q + 3]), rr), f.y));
-                        }
+                        for (int q = 0; q < 8; ++q) out[q] = 0;
                     } else {
-                        // keys that this row may use: live and, on the diagonal block, not
-                        // on the wrong side of the row
-                        uint32_t use = live;
-                        if (b == w) use &= kRev ? 0xffffffffu << lane : 0xffffffffu >> (31 - lane);
-                        float v[32];
-                        tmem_ld32(tp + 32 * b, v);
-                        tmem_ld_wait();
-                        const uint64_t sign = kRev ? pair2(1.f, 1.f) : pair2(-1.f, -1.f);
-                        const uint64_t cc = kRev ? pair2(-ct, -ct) : pair2(ct, ct);
-                        const uint64_t ps = pair2(p.pair_scale, p.pair_scale);
+                        float v[16];
+                        tmem_ld16(tp + col, v);
+                        const uint32_t live = sc->live[b];
+                        if (b != w && live == 0xffffffffu) {
+                            // token to its block's border to this row: both exponents <= 0
+                            const float border = sc->c[kRev ? 32 * b : 32 * b + 31];
+                            const float r = p.pair_scale * ex2(kRev ? border - ct : ct - border);
+                            const uint64_t rr = pair2(r, r);
+                            tmem_ld_wait();
 #pragma unroll
-                        for (int q = 0; q < 32; q += 2) {
-                            const uint64_t c2 =
-                                *reinterpret_cast<const uint64_t*>(&sc->c[32 * b + q]);
-                            float ea, eb, a, d;
-                            split2(fma2(c2, sign, cc), ea, eb);
-                            split2(mul2(mul2(pair2(v[q], v[q + 1]), ps), pair2(ex2(ea), ex2(eb))), a, d);
-                            out[q / 2] =
-                                pack_bf16((use >> q) & 1 ? a : 0.f, (use >> (q + 1)) & 1 ? d : 0.f);
+                            for (int q = 0; q < 16; q += 4) {
+                                const ulonglong2 f =
+                                    *reinterpret_cast<const ulonglong2*>(&sc->f[col + q]);
+                                out[q / 2] = pack2(mul2(mul2(pair2(v[q], v[q + 1]), rr), f.x));
+                                out[q / 2 + 1] = pack2(mul2(mul2(pair2(v[q + 2], v[q + 3]), rr), f.y));
+                            }
+                        } else {
+                            // keys that this row may use: live and, on the diagonal block, not
+                            // on the wrong side of the row
+                            uint32_t use = live;
+                            if (b == w) use &= kRev ? 0xffffffffu << lane : 0xffffffffu >> (31 - lane);
+                            use >>= col & 16;
+                            const uint64_t sign = kRev ? pair2(1.f, 1.f) : pair2(-1.f, -1.f);
+                            const uint64_t cc = kRev ? pair2(-ct, -ct) : pair2(ct, ct);
+                            const uint64_t ps = pair2(p.pair_scale, p.pair_scale);
+                            tmem_ld_wait();
+#pragma unroll
+                            for (int q = 0; q < 16; q += 2) {
+                                const uint64_t c2 = *reinterpret_cast<const uint64_t*>(&sc->c[col + q]);
+                                float ea, eb, a, d;
+                                split2(fma2(c2, sign, cc), ea, eb);
+                                split2(mul2(mul2(pair2(v[q], v[q + 1]), ps), pair2(ex2(ea), ex2(eb))), a,
+                                       d);
+                                out[q / 2] = pack_bf16((use >> q) & 1 ? a : 0.f,
+                                                       (use >> (q + 1)) & 1 ? d : 0.f);
+                            }
                         }
                     }
-                    // in place: block b's 16 columns lie over scores that are read already
-                    tmem_st_raw16(tp + 16 * b, out);
+                    // in place: these 8 columns lie over scores that are read already
+                    tmem_st_raw8(tp + 8 * hb, out);
                 }
                 tmem_st_wait();
                 tc_fence_before();
@@ -989,12 +986,14 @@ la_chunked_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constan
                                     pack_bf16(S[8 * q + 4], S[8 * q + 5]),
                                     pack_bf16(S[8 * q + 6], S[8 * q + 7]));
                 } else {
+                    // blocks (rows 16 w .., columns 8 c ..), (rows + 8, same), (.., next c), ..
+                    const int r = 16 * w + (lane & 15);
 #pragma unroll
-                    for (int m = 0; m < R / 2; ++m) {
-                        const int r = srow + 8 * (m & 1);
-                        st_shared4(state_s + r * 128 + (((m / 2) ^ (r & 7)) << 4) + 4 * (lane & 3),
-                                   pack_bf16(S[2 * m], S[2 * m + 1]));
-                    }
+                    for (int c = 0; c < 8; c += 2)
+                        stmatrix4(state_s + r * 128 + (((c + (lane >> 4)) ^ (r & 7)) << 4),
+                                  pack_bf16(S[4 * c], S[4 * c + 1]), pack_bf16(S[4 * c + 2], S[4 * c + 3]),
+                                  pack_bf16(S[4 * c + 4], S[4 * c + 5]),
+                                  pack_bf16(S[4 * c + 6], S[4 * c + 7]));
                 }
                 fence_proxy_async();
             }
@@ -1137,18 +1136,12 @@ la_chunked_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constan
                     const long long grow = rw.first + (long long)t * rw.step;
                     const uint32_t to = tmem + ((uint32_t)(32 * w) << 16);
                     float dot = 0.f;
-                    // 32 columns at a time where registers allow (no state beside them)
-                    constexpr int V = kBoth ? 16 : 32;
+                    constexpr int V = 16;
 #pragma unroll 1
                     for (int q = 0; q < D; q += V) {
                         float ox[V], oi[V];
-                        if constexpr (kBoth) {
-                            tmem_ld16(to + C::TM_OX + q, ox);
-                            tmem_ld16(to + C::TM_OI + q, oi);
-                        } else {
-                            tmem_ld32(to + C::TM_OX + q, ox);
-                            tmem_ld32(to + C::TM_OI + q, oi);
-                        }
+                        tmem_ld16(to + C::TM_OX + q, ox);
+                        tmem_ld16(to + C::TM_OI + q, oi);
                         uint4 wv[V / 8];
                         if (kGrad && in && row_out) {
                             const uint4* src =
