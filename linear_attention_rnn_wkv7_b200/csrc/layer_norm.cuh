@@ -7,13 +7,15 @@
 // head: the norm of a mixing layer's output): row r is of group (r / inner) % G, inner = 1
 // for [.., G, D] rows and T for head-first [B, G, T, D] ones.
 //
-// Bound by HBM: x once in and y once out (x, dy in, dx out).  A team of threads holds a
-// row in registers, so the variance is summed around the mean (no cancellation of two
-// large sums) without a second read.  Team t works on rows of group t % G only: w and b stay in
-// registers over its rows, and in the backward so do its sums of dw and db, written once at
-// the end; a second kernel adds the teams' sums in a fixed order (no atomics: the result
-// does not depend on scheduling).  Consecutive teams hold consecutive groups, so a block's
-// loads are contiguous for every layout with inner = 1.
+// Bound by HBM: x once in and y once out (x, dy in, dx out).  A team of threads holds a row
+// in registers, while the next one's loads are already in flight.  Statistics take one
+// exchange: each thread has the mean and the sum of squares around it of its own
+// elements, and pairs merge as (n, m, M2): m += d n2 / n12, M2 += M2' + d^2 n1 n2 / n12 with d
+// the means' difference (no cancellation of two large sums, no second read).  Team t works on
+// rows of group t % G only: w and b stay in registers over its rows, and in the backward so do
+// its sums of dw and db, written once at the end; a second kernel adds the teams' sums in a
+// fixed order (no atomics: the result does not depend on scheduling).  Consecutive teams
+// hold consecutive groups, so a block's loads are contiguous for every layout with inner = 1.
 //
 // All statistics and sums are fp32.  Above 8192 elements the backward's registers no longer
 // hold a row and its sums of dw and db, so those get a kernel of their own, which reads x
@@ -89,6 +91,41 @@ template <int VEC> __device__ __forceinline__ void store(__nv_bfloat16* p, const
     }
 }
 
+// VEC elements as they are in memory (prefetched rows), and as fp32.
+template <typename T, int VEC> struct Raw { T v[VEC]; };
+template <> struct Raw<__nv_bfloat16, 8> { uint4 v; };
+template <> struct Raw<__nv_bfloat16, 4> { uint2 v; };
+template <> struct Raw<float, 8> { float4 v[2]; };
+template <> struct Raw<float, 4> { float4 v; };
+template <typename T, int VEC> __device__ __forceinline__ Raw<T, VEC> load_raw(const T* p) {
+    return *reinterpret_cast<const Raw<T, VEC>*>(p);
+}
+template <int VEC> __device__ __forceinline__ void unpack(const Raw<float, VEC>& r, float (&v)[VEC]) {
+    if constexpr (VEC == 8) {
+        v[0] = r.v[0].x; v[1] = r.v[0].y; v[2] = r.v[0].z; v[3] = r.v[0].w;
+        v[4] = r.v[1].x; v[5] = r.v[1].y; v[6] = r.v[1].z; v[7] = r.v[1].w;
+    } else if constexpr (VEC == 4) {
+        v[0] = r.v.x; v[1] = r.v.y; v[2] = r.v.z; v[3] = r.v.w;
+    } else {
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) v[i] = r.v[i];
+    }
+}
+template <int VEC>
+__device__ __forceinline__ void unpack(const Raw<__nv_bfloat16, VEC>& r, float (&v)[VEC]) {
+    if constexpr (VEC == 8) {
+        const uint32_t w[4] = {r.v.x, r.v.y, r.v.z, r.v.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            v[2 * i] = __uint_as_float(w[i] << 16);
+            v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) v[i] = __bfloat162float(r.v[i]);
+    }
+}
+
 // Sums of NS values over a team of TPR threads (a power of two; several teams a block when
 // TPR <= 32; above it the block is one team).  Every thread gets the sums.
 template <int TPR, int NS>
@@ -116,81 +153,158 @@ __device__ __forceinline__ void team_sum(float (&s)[NS], float (*red)[32]) {
     }
 }
 
+// Merging (n, mean, M2) over a team: the counts are the same for every row, so each level's
+// n2 / n12 and n1 n2 / n12 are made once.
+template <int TPR>
+struct Merge {
+    static constexpr int kIn = TPR < 32 ? TPR : 32, kWarps = TPR / 32;
+    static constexpr int levels(int n) { return n <= 1 ? 0 : 1 + levels(n / 2); }
+    static constexpr int kA = levels(kIn), kB = levels(kWarps);
+    float r[kA + kB + 1], c[kA + kB + 1];
+
+    __device__ __forceinline__ void level(float& n, int l, int m) {
+        const float n2 = __shfl_xor_sync(0xffffffffu, n, m), tot = n + n2;
+        r[l] = tot > 0.f ? n2 / tot : 0.f;
+        c[l] = n * r[l];
+        n = tot;
+    }
+    __device__ __forceinline__ explicit Merge(float n, float* red) {
+#pragma unroll
+        for (int l = 0; l < kA; ++l) level(n, l, 1 << l);
+        if constexpr (TPR > 32) {
+            const int lane = threadIdx.x & 31;
+            if (lane == 0) red[threadIdx.x >> 5] = n;
+            __syncthreads();
+            n = lane < kWarps ? red[lane] : 0.f;
+#pragma unroll
+            for (int l = 0; l < kB; ++l) level(n, kA + l, 1 << l);
+            __syncthreads();
+        }
+    }
+    __device__ __forceinline__ void merge(float& mean, float& m2, int l, int m) const {
+        const float d = __shfl_xor_sync(0xffffffffu, mean, m) - mean;
+        m2 += __shfl_xor_sync(0xffffffffu, m2, m);
+        mean = fmaf(d, r[l], mean);
+        m2 = fmaf(d * d, c[l], m2);
+    }
+    // Mean and sum of squares around it over the team, from each thread's; all get the same.
+    __device__ __forceinline__ void operator()(float& mean, float& m2, float (*red)[32]) const {
+#pragma unroll
+        for (int l = 0; l < kA; ++l) merge(mean, m2, l, 1 << l);
+        const int lane = threadIdx.x & 31;
+        if constexpr (TPR > 32) {
+            const int warp = threadIdx.x >> 5;
+            if (lane == 0) {
+                red[0][warp] = mean;
+                red[1][warp] = m2;
+            }
+            __syncthreads();
+            mean = lane < kWarps ? red[0][lane] : 0.f;
+            m2 = lane < kWarps ? red[1][lane] : 0.f;
+#pragma unroll
+            for (int l = 0; l < kB; ++l) merge(mean, m2, kA + l, 1 << l);
+        }
+        // (the two lanes of a merge may differ in its last bit)
+        mean = __shfl_sync(0xffffffffu, mean, TPR >= 32 ? 0 : lane & ~(TPR - 1));
+        m2 = __shfl_sync(0xffffffffu, m2, TPR >= 32 ? 0 : lane & ~(TPR - 1));
+    }
+};
+
 // Threads of a block.
 template <int TPR> constexpr int block_threads() { return TPR <= 32 ? 128 : TPR; }
+// Blocks per SM, by the registers that a row of N elements a thread, the next one, the weights and
+// (backward) the sums of dw and db take.
+template <int TPR, int N> constexpr int fwd_blocks() {
+    constexpr int threads = N <= 8 ? 1536 : N <= 16 ? 1024 : 512;
+    return threads / block_threads<TPR>() > 0 ? threads / block_threads<TPR>() : 1;
+}
+template <int TPR, int N> constexpr int bwd_blocks() {
+    constexpr int threads = N <= 8 ? 768 : 512;
+    return threads / block_threads<TPR>() > 0 ? threads / block_threads<TPR>() : 1;
+}
 
-// A team of TPR threads holds NI groups of VEC elements a thread.  kTail: D is not a
-// multiple of TPR * VEC * NI (groups past D are skipped; VEC divides D).
+// A team of TPR threads holds NI groups of VEC elements a thread (groups past D are skipped;
+// VEC divides D).
 template <typename T, typename Tw, int TPR, int NI, int VEC>
-__global__ void __launch_bounds__(block_threads<TPR>())
+__global__ void __launch_bounds__(block_threads<TPR>(), fwd_blocks<TPR, NI * VEC>())
 ln_fwd_kernel(const T* __restrict__ x, const Tw* __restrict__ w, const Tw* __restrict__ b,
               T* __restrict__ y, float* __restrict__ mean, float* __restrict__ rstd, Shape s) {
-    __shared__ float red[2][1][32];
+    __shared__ float red[2][2][32];
+    constexpr int kTeams = block_threads<TPR>() / TPR;
     const int lane = threadIdx.x % TPR;
-    const long long team = (long long)blockIdx.x * (block_threads<TPR>() / TPR) + threadIdx.x / TPR;
+    const long long team = (long long)blockIdx.x * kTeams + threadIdx.x / TPR;
     const bool in = team < s.teams;
     const int group = in ? (int)(team % s.G) : 0;
     const long long per = s.rows / s.G, step = s.teams / s.G;
-    const float inv = 1.f / (float)s.D;
     // Every team of a block runs as many turns as its first (whole warps stay together
     // for the shuffles); rows past the end are not loaded or stored.
     const long long first = in ? team / s.G : 0;
-    const long long turns =
-        (per - (long long)blockIdx.x * (block_threads<TPR>() / TPR) / s.G + step - 1) / step;
-    float xr[NI][VEC];
-    auto fetch = [&](long long k, float (&dst)[NI][VEC]) {
-        const bool ok = in && k < per;
-        const T* px = x + (ok ? row_at(s, k, group) : 0) * s.D;
+    const long long turns = (per - (long long)blockIdx.x * kTeams / s.G + step - 1) / step;
+    const long long wo = (long long)group * s.D;
+    float count = 0.f;
+    Raw<T, VEC> next[NI];
+    Raw<Tw, VEC> wr[NI], br[NI];
+#pragma unroll
+    for (int i = 0; i < NI; ++i) {
+        const int e = (i * TPR + lane) * VEC;
+        if (e < s.D) {
+            count += (float)VEC;
+            if (w) wr[i] = load_raw<Tw, VEC>(w + wo + e);
+            if (b) br[i] = load_raw<Tw, VEC>(b + wo + e);
+        }
+    }
+    auto fetch = [&](long long k) {
+        if (!in || k >= per) return;
+        const T* px = x + row_at(s, k, group) * s.D;
 #pragma unroll
         for (int i = 0; i < NI; ++i) {
             const int e = (i * TPR + lane) * VEC;
-            if (ok && e < s.D) {
-                load<VEC>(px + e, dst[i]);
-            } else {
-#pragma unroll
-                for (int q = 0; q < VEC; ++q) dst[i][q] = 0.f;
-            }
+            if (e < s.D) next[i] = load_raw<T, VEC>(px + e);
         }
     };
+    const float inv_n = count > 0.f ? 1.f / count : 0.f, inv_d = 1.f / (float)s.D;
+    fetch(first);
+    const Merge<TPR> merge(count, red[0][0]);
     long long k = first;
     for (long long turn = 0; turn < turns; ++turn, k += step) {
-        fetch(k, xr);
         const bool ok = in && k < per;
-        float a[1] = {0.f};
-#pragma unroll
-        for (int i = 0; i < NI; ++i)
-#pragma unroll
-            for (int q = 0; q < VEC; ++q) a[0] += xr[i][q];
-        team_sum<TPR, 1>(a, red[0]);
-        const float m = a[0] * inv;
-        a[0] = 0.f;
+        float xr[NI][VEC], m = 0.f, m2 = 0.f;
 #pragma unroll
         for (int i = 0; i < NI; ++i) {
-            const int e = (i * TPR + lane) * VEC;
-            if (e < s.D) {
+            const bool live = ok && (i * TPR + lane) * VEC < s.D;
+            if (live) {
+                unpack<VEC>(next[i], xr[i]);
+            } else {
 #pragma unroll
-                for (int q = 0; q < VEC; ++q) {
-                    xr[i][q] -= m;
-                    a[0] = fmaf(xr[i][q], xr[i][q], a[0]);
-                }
+                for (int q = 0; q < VEC; ++q) xr[i][q] = 0.f;
+            }
+#pragma unroll
+            for (int q = 0; q < VEC; ++q) m += xr[i][q];
+        }
+        fetch(k + step);
+        m *= inv_n;
+#pragma unroll
+        for (int i = 0; i < NI; ++i) {
+            if ((i * TPR + lane) * VEC < s.D) {
+#pragma unroll
+                for (int q = 0; q < VEC; ++q) m2 = fmaf(xr[i][q] - m, xr[i][q] - m, m2);
             }
         }
-        team_sum<TPR, 1>(a, red[1]);
-        const float r = 1.f / sqrtf(a[0] * inv + s.eps);
+        merge(m, m2, red[turn & 1]);
+        const float r = 1.f / sqrtf(m2 * inv_d + s.eps);
         if (ok) {
             const long long row = row_at(s, k, group);
             T* py = y + row * s.D;
-            const long long wo = (long long)group * s.D;
 #pragma unroll
             for (int i = 0; i < NI; ++i) {
                 const int e = (i * TPR + lane) * VEC;
                 if (e < s.D) {
                     float wv[VEC], bv[VEC];
-                    if (w) load<VEC>(w + wo + e, wv);
-                    if (b) load<VEC>(b + wo + e, bv);
+                    if (w) unpack<VEC>(wr[i], wv);
+                    if (b) unpack<VEC>(br[i], bv);
 #pragma unroll
                     for (int q = 0; q < VEC; ++q) {
-                        float v = xr[i][q] * r;
+                        float v = (xr[i][q] - m) * r;
                         if (w) v *= wv[q];
                         if (b) v += bv[q];
                         xr[i][q] = v;
@@ -206,49 +320,75 @@ ln_fwd_kernel(const T* __restrict__ x, const Tw* __restrict__ w, const Tw* __res
     }
 }
 
-// part: [S][2][G][D] with S = teams / G, the teams' sums of dy xh and of dy.
-template <typename T, typename Tw, int TPR, int NI, int VEC, bool kParam>
-__global__ void __launch_bounds__(block_threads<TPR>())
+// part: [S][2][G][D], the sums of dy xh and of dy of S = teams / G teams a group, or with
+// kBlockSum (one group, several teams a block) of S = blocks.
+template <typename T, typename Tw, int TPR, int NI, int VEC, bool kParam, bool kBlockSum>
+__global__ void __launch_bounds__(block_threads<TPR>(), bwd_blocks<TPR, NI * VEC>())
 ln_bwd_kernel(const T* __restrict__ x, const T* __restrict__ dy, const float* __restrict__ mean,
               const float* __restrict__ rstd, const Tw* __restrict__ w, T* __restrict__ dx,
               float* __restrict__ part, Shape s) {
     __shared__ float red[2][2][32];
+    constexpr int kTeams = block_threads<TPR>() / TPR;
+    // (1024 threads have 64 registers each: no room for the next row beside a long one)
+    constexpr bool kPrefetch = TPR < 1024 || NI * VEC <= 8;
     const int lane = threadIdx.x % TPR;
-    const long long team = (long long)blockIdx.x * (block_threads<TPR>() / TPR) + threadIdx.x / TPR;
+    const long long team = (long long)blockIdx.x * kTeams + threadIdx.x / TPR;
     const bool in = team < s.teams;
     const int group = in ? (int)(team % s.G) : 0;
     const long long per = s.rows / s.G, step = s.teams / s.G;
     const float inv = 1.f / (float)s.D;
     const long long first = in ? team / s.G : 0;
-    const long long turns =
-        (per - (long long)blockIdx.x * (block_threads<TPR>() / TPR) / s.G + step - 1) / step;
+    const long long turns = (per - (long long)blockIdx.x * kTeams / s.G + step - 1) / step;
     const long long wo = (long long)group * s.D;
     float dw[kParam ? NI : 1][VEC], db[kParam ? NI : 1][VEC];
 #pragma unroll
     for (int i = 0; i < (kParam ? NI : 1); ++i)
 #pragma unroll
         for (int q = 0; q < VEC; ++q) dw[i][q] = db[i][q] = 0.f;
+    Raw<Tw, VEC> wr[NI];
+    Raw<T, VEC> nx[NI], nd[NI];
+    float nm = 0.f, nr = 0.f;
+#pragma unroll
+    for (int i = 0; i < NI; ++i) {
+        const int e = (i * TPR + lane) * VEC;
+        if (kPrefetch && w && e < s.D) wr[i] = load_raw<Tw, VEC>(w + wo + e);
+    }
+    auto fetch = [&](long long k) {
+        if (!in || k >= per) return;
+        const long long row = row_at(s, k, group);
+        nm = mean[row];
+        nr = rstd[row];
+#pragma unroll
+        for (int i = 0; i < NI; ++i) {
+            const int e = (i * TPR + lane) * VEC;
+            if (e < s.D) {
+                nx[i] = load_raw<T, VEC>(x + row * s.D + e);
+                nd[i] = load_raw<T, VEC>(dy + row * s.D + e);
+            }
+        }
+    };
+    if (kPrefetch) fetch(first);
     long long k = first;
     for (long long turn = 0; turn < turns; ++turn, k += step) {
         const bool ok = in && k < per;
-        const long long row = ok ? row_at(s, k, group) : 0;
-        const float m = ok ? mean[row] : 0.f, r = ok ? rstd[row] : 0.f;
+        if (!kPrefetch) fetch(k);
+        const float m = nm, r = nr;
         float xh[NI][VEC], u[NI][VEC];
         float a[2] = {0.f, 0.f};
 #pragma unroll
         for (int i = 0; i < NI; ++i) {
-            const int e = (i * TPR + lane) * VEC;
-            if (ok && e < s.D) {
-                load<VEC>(x + row * s.D + e, xh[i]);
-                load<VEC>(dy + row * s.D + e, u[i]);
+            if (ok && (i * TPR + lane) * VEC < s.D) {
+                unpack<VEC>(nx[i], xh[i]);
+                unpack<VEC>(nd[i], u[i]);
             }
         }
+        if (kPrefetch) fetch(k + step);
 #pragma unroll
         for (int i = 0; i < NI; ++i) {
-            const int e = (i * TPR + lane) * VEC;
-            if (ok && e < s.D) {
+            if (ok && (i * TPR + lane) * VEC < s.D) {
                 float wv[VEC];
-                if (w) load<VEC>(w + wo + e, wv);
+                if (w && !kPrefetch) wr[i] = load_raw<Tw, VEC>(w + wo + (i * TPR + lane) * VEC);
+                if (w) unpack<VEC>(wr[i], wv);
 #pragma unroll
                 for (int q = 0; q < VEC; ++q) {
                     xh[i][q] = (xh[i][q] - m) * r;
@@ -265,27 +405,55 @@ ln_bwd_kernel(const T* __restrict__ x, const T* __restrict__ dy, const float* __
         team_sum<TPR, 2>(a, red[turn & 1]);
         const float c0 = a[0] * inv, c1 = a[1] * inv;
         if (ok) {
+            T* pd = dx + row_at(s, k, group) * s.D;
 #pragma unroll
             for (int i = 0; i < NI; ++i) {
                 const int e = (i * TPR + lane) * VEC;
                 if (e < s.D) {
 #pragma unroll
                     for (int q = 0; q < VEC; ++q) xh[i][q] = r * (u[i][q] - c0 - xh[i][q] * c1);
-                    store<VEC>(dx + row * s.D + e, xh[i]);
+                    store<VEC>(pd + e, xh[i]);
                 }
             }
         }
     }
-    if (kParam && in) {
+    if constexpr (kParam && kBlockSum) {
+        // the block's teams, in order, through shared memory
+        __shared__ float sums[2][kTeams][TPR * NI * VEC];
+        const int t = threadIdx.x / TPR;
+#pragma unroll
+        for (int i = 0; i < NI; ++i)
+#pragma unroll
+            for (int q = 0; q < VEC; ++q) {
+                sums[0][t][(i * TPR + lane) * VEC + q] = dw[i][q];
+                sums[1][t][(i * TPR + lane) * VEC + q] = db[i][q];
+            }
+        __syncthreads();
+        float* p = part + (long long)blockIdx.x * 2 * s.D;
+        for (int e = threadIdx.x; e < 2 * s.D; e += block_threads<TPR>()) {
+            const int which = e >= s.D, c = which ? e - s.D : e;
+            float a = 0.f;
+#pragma unroll
+            for (int j = 0; j < kTeams; ++j) a += sums[which][j][c];
+            p[e] = a;
+        }
+    } else if (kParam && in) {
         float* p = part + (team / s.G) * 2 * s.G * s.D + wo;
 #pragma unroll
         for (int i = 0; i < NI; ++i) {
             const int e = (i * TPR + lane) * VEC;
             if (e < s.D) {
+                if constexpr (VEC == 1) {
+                    p[e] = dw[i][0];
+                    p[(long long)s.G * s.D + e] = db[i][0];
+                } else {
 #pragma unroll
-                for (int q = 0; q < VEC; ++q) {
-                    p[e + q] = dw[i][q];
-                    p[(long long)s.G * s.D + e + q] = db[i][q];
+                    for (int q = 0; q < VEC; q += 4) {
+                        *reinterpret_cast<float4*>(p + e + q) =
+                            make_float4(dw[i][q], dw[i][q + 1], dw[i][q + 2], dw[i][q + 3]);
+                        *reinterpret_cast<float4*>(p + (long long)s.G * s.D + e + q) =
+                            make_float4(db[i][q], db[i][q + 1], db[i][q + 2], db[i][q + 3]);
+                    }
                 }
             }
         }
@@ -336,6 +504,7 @@ ln_param_kernel(const float* __restrict__ part, long long S, long long cols, Tw*
     const long long c = (long long)blockIdx.x * 32 + lane;  // 2 * cols columns
     float a = 0.f;
     if (c < 2 * cols)
+#pragma unroll 8
         for (long long i = warp; i < S; i += 8) a += part[i * 2 * cols + c];
     red[warp][lane] = a;
     __syncthreads();
@@ -359,11 +528,11 @@ constexpr int kMaxD = 1 << 15;
 struct Launch {
     long long blocks, teams;
 };
-// Teams: as many as fill the GPU a few times over, a multiple of G, at most one per row.
+// Teams: as many as the GPU holds at once (per_sm blocks), a multiple of G, at most one per row.
 inline Launch plan(long long rows, int G, int tpr, int threads, int per_sm) {
     const long long per = rows / G;
     const int tpb = threads / tpr;
-    const long long want = (long long)148 * per_sm * tpb;  // resident teams
+    const long long want = (long long)148 * per_sm * tpb;
     long long S = (want + G - 1) / G;
     if (S > per) S = per;
     if (S < 1) S = 1;
@@ -413,7 +582,7 @@ inline cudaError_t launch_fwd(const T* x, const Tw* w, const Tw* b, T* y, float*
     return with_team<16 / sizeof(T)>(D, [&](auto cfg) {
         using C = decltype(cfg);
         constexpr int threads = block_threads<C::TPR>();
-        const Launch l = plan(rows, G, C::TPR, threads, 2048 / threads);
+        const Launch l = plan(rows, G, C::TPR, threads, fwd_blocks<C::TPR, C::NI * C::VEC>());
         Shape s{rows, inner, G, D, l.teams, eps};
         ln_fwd_kernel<T, Tw, C::TPR, C::NI, C::VEC>
             <<<(unsigned)l.blocks, threads, 0, stream>>>(x, w, b, y, mean, rstd, s);
@@ -433,7 +602,8 @@ inline long long bwd_parts(long long rows, int G, int D) {
     (void)with_team<16 / sizeof(T)>(D, [&](auto cfg) {
         using C = decltype(cfg);
         constexpr int threads = block_threads<C::TPR>();
-        S = plan(rows, G, C::TPR, threads, 1024 / threads).teams / G;
+        const Launch l = plan(rows, G, C::TPR, threads, bwd_blocks<C::TPR, C::NI * C::VEC>());
+        S = G == 1 ? l.blocks : l.teams / G;
         return cudaSuccess;
     });
     return S;
@@ -448,17 +618,22 @@ inline cudaError_t launch_bwd(const T* x, const T* dy, const float* mean, const 
     const cudaError_t e = with_team<16 / sizeof(T)>(D, [&](auto cfg) {
         using C = decltype(cfg);
         constexpr int threads = block_threads<C::TPR>();
-        const Launch l = plan(rows, G, C::TPR, threads, 1024 / threads);
+        const Launch l = plan(rows, G, C::TPR, threads, bwd_blocks<C::TPR, C::NI * C::VEC>());
         Shape s{rows, inner, G, D, l.teams, 0.f};
+        const dim3 grid((unsigned)l.blocks);
         if constexpr (C::TPR * C::NI * C::VEC <= kMaxFusedD) {
             if (param) {
-                ln_bwd_kernel<T, Tw, C::TPR, C::NI, C::VEC, true>
-                    <<<(unsigned)l.blocks, threads, 0, stream>>>(x, dy, mean, rstd, w, dx, part, s);
+                if (C::TPR <= 32 && G == 1)  // (above 32 a block is one team)
+                    ln_bwd_kernel<T, Tw, C::TPR, C::NI, C::VEC, true, (C::TPR <= 32)>
+                        <<<grid, threads, 0, stream>>>(x, dy, mean, rstd, w, dx, part, s);
+                else
+                    ln_bwd_kernel<T, Tw, C::TPR, C::NI, C::VEC, true, false>
+                        <<<grid, threads, 0, stream>>>(x, dy, mean, rstd, w, dx, part, s);
                 return cudaGetLastError();
             }
         }
-        ln_bwd_kernel<T, Tw, C::TPR, C::NI, C::VEC, false>
-            <<<(unsigned)l.blocks, threads, 0, stream>>>(x, dy, mean, rstd, w, dx, part, s);
+        ln_bwd_kernel<T, Tw, C::TPR, C::NI, C::VEC, false, false>
+            <<<grid, threads, 0, stream>>>(x, dy, mean, rstd, w, dx, part, s);
         return cudaGetLastError();
     });
     if (e != cudaSuccess || !param) return e;

@@ -8,7 +8,8 @@ from __future__ import annotations
 import torch
 from torch.autograd.function import once_differentiable
 
-from .wkv7 import OK, WKV7Error, _check, _dtype_code, _ptr, _stream, library
+from ._args import address, expect, on_device, stream
+from .wkv7 import OK, WKV7Error, _check, _dtype_code, library
 
 
 def _groups(x, params, head_first):
@@ -18,30 +19,26 @@ def _groups(x, params, head_first):
     if x.dim() < 1 or x.shape[-1] == 0:
         raise ValueError(f"x must have rows of 1 or more elements, got {tuple(x.shape)}")
     D = x.shape[-1]
-    given = {n: t for n, t in params.items() if t is not None}
-    shapes = {tuple(t.shape) for t in given.values()}
-    dtypes = {t.dtype for t in given.values()}
-    if len(shapes) > 1 or len(dtypes) > 1:
-        raise ValueError(f"{', '.join(given)} must have one shape and one dtype")
-    groups, inner = 1, 1
-    wdtype = dtypes.pop() if dtypes else x.dtype
-    if shapes:
-        shape = shapes.pop()
-        if len(shape) == 2:  # one weight and bias for each head
-            groups = shape[0]
-            if head_first:
-                ok = x.dim() == 4 and x.shape[1] == groups
-                inner = x.shape[2] if ok else 1
-            else:
-                ok = x.dim() >= 2 and x.shape[-2] == groups
-            if not ok or groups == 0:
-                raise ValueError(f"weight and bias {shape} do not fit x {tuple(x.shape)}")
-        for n, t in given.items():
-            _check(t, n, wdtype, (D,) if len(shape) != 2 else (groups, D))
-            if t.device != x.device:
-                raise ValueError(f"{n} is on {t.device}, x on {x.device}: one device only")
-        if wdtype not in (torch.float32, x.dtype):
-            raise TypeError(f"weights must be float32 or {x.dtype}, got {wdtype}")
+    groups, inner, shape, wdtype = 1, 1, None, x.dtype
+    for n, t in params:
+        if t is None:
+            continue
+        if shape is None:
+            shape, wdtype = t.shape, t.dtype
+            if len(shape) == 2:  # one weight and bias for each head
+                groups = shape[0]
+                if head_first:
+                    ok = x.dim() == 4 and x.shape[1] == groups
+                    inner = x.shape[2] if ok else 1
+                else:
+                    ok = x.dim() >= 2 and x.shape[-2] == groups
+                if not ok or groups == 0:
+                    raise ValueError(f"{n} {tuple(shape)} does not fit x {tuple(x.shape)}")
+            if wdtype is not x.dtype and wdtype is not torch.float32:
+                raise TypeError(f"{n} must be float32 or {x.dtype}, got {wdtype}")
+            expect(t, n, wdtype, (groups, D) if len(shape) == 2 else (D,), x)
+        else:
+            expect(t, n, wdtype, shape, x)
     return x.numel() // D, groups, max(inner, 1), D, wdtype
 
 
@@ -53,19 +50,17 @@ def wkv7_ln_fwd(x, weight=None, bias=None, eps: float = 1e-5, head_first: bool =
     """Layer norm over the last dimension.  x [..., D] bf16 or fp32; weight, bias [D], or [H, D] for
     one of each head of x [..., H, D] (with head_first: of x [B, H, T, D]), in x's dtype or
     fp32, or None.  Returns (y, mean, rstd); the fp32 statistics have x's leading shape."""
-    rows, groups, inner, D, wdtype = _groups(x, {"weight": weight, "bias": bias}, head_first)
+    rows, groups, inner, D, wdtype = _groups(x, (("weight", weight), ("bias", bias)), head_first)
     if y is None:
         y = torch.empty_like(x)
     else:
-        _check(y, "y", x.dtype, x.shape)
-        if y.device != x.device:
-            raise ValueError(f"y is on {y.device}, x on {x.device}: one device only")
+        expect(y, "y", x.dtype, x.shape, x)
     mean = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device)
     rstd = torch.empty_like(mean)
-    with torch.cuda.device(x.device):
-        st = library().wkv7_ln_fwd(_ptr(x), _ptr(weight), _ptr(bias), _ptr(y), _ptr(mean),
-                                   _ptr(rstd), rows, groups, inner, D, float(eps),
-                                   _dtype_code(x), _code(wdtype), _stream(x.device))
+    with on_device(x):
+        st = library().wkv7_ln_fwd(address(x), address(weight), address(bias), address(y), address(mean),
+                                   address(rstd), rows, groups, inner, D, float(eps),
+                                   _dtype_code(x), _code(wdtype), stream(x))
     if st != OK:
         raise WKV7Error(st, "wkv7_ln_fwd")
     return y, mean, rstd
@@ -76,13 +71,10 @@ def wkv7_ln_bwd(x, dy, mean, rstd, weight=None, head_first: bool = False, need_p
     """Backward of wkv7_ln_fwd for L = sum(y * dy), with the forward's mean and rstd.  Returns a
     dict: dx, dweight, dbias (shaped like weight and in its dtype; None when there is no
     weight).  need_params False leaves dweight and dbias out."""
-    rows, groups, inner, D, wdtype = _groups(x, {"weight": weight}, head_first)
-    _check(dy, "dy", x.dtype, x.shape)
-    _check(mean, "mean", torch.float32, x.shape[:-1])
-    _check(rstd, "rstd", torch.float32, x.shape[:-1])
-    for n, t in (("dy", dy), ("mean", mean), ("rstd", rstd), ("workspace", workspace)):
-        if t is not None and t.device != x.device:
-            raise ValueError(f"{n} is on {t.device}, x on {x.device}: one device only")
+    rows, groups, inner, D, wdtype = _groups(x, (("weight", weight),), head_first)
+    expect(dy, "dy", x.dtype, x.shape, x)
+    expect(mean, "mean", torch.float32, x.shape[:-1], x)
+    expect(rstd, "rstd", torch.float32, x.shape[:-1], x)
     need = (weight is not None) if need_params is None else bool(need_params)
     if need and weight is None:
         raise ValueError("need_params needs the weight")
@@ -90,16 +82,16 @@ def wkv7_ln_bwd(x, dy, mean, rstd, weight=None, head_first: bool = False, need_p
     dw = torch.empty_like(weight) if need else None
     db = torch.empty_like(weight) if need else None
     lib = library()
-    with torch.cuda.device(x.device):
+    with on_device(x):
         nbytes = int(lib.wkv7_ln_bwd_workspace_bytes(rows, groups, inner, D, _dtype_code(x)))
         if workspace is not None:
-            _check(workspace, "workspace", torch.uint8)
+            expect(workspace, "workspace", torch.uint8, workspace.shape, x)
         elif need and nbytes:
             workspace = torch.empty(nbytes, dtype=torch.uint8, device=x.device)
-        st = lib.wkv7_ln_bwd(_ptr(x), _ptr(dy), _ptr(mean), _ptr(rstd), _ptr(weight), _ptr(dx),
-                             _ptr(dw), _ptr(db), rows, groups, inner, D, _dtype_code(x),
-                             _code(wdtype), _ptr(workspace),
-                             0 if workspace is None else workspace.numel(), _stream(x.device))
+        st = lib.wkv7_ln_bwd(address(x), address(dy), address(mean), address(rstd), address(weight), address(dx),
+                             address(dw), address(db), rows, groups, inner, D, _dtype_code(x),
+                             _code(wdtype), address(workspace),
+                             0 if workspace is None else workspace.numel(), stream(x))
     if st != OK:
         raise WKV7Error(st, "wkv7_ln_bwd")
     return {"dx": dx, "dweight": dw, "dbias": db}

@@ -11,13 +11,8 @@ from __future__ import annotations
 import torch
 from torch.autograd.function import once_differentiable
 
-from .wkv7 import ALGO, OK, WKV7Error, _check, _dtype_code, _head_norm, _ptr, _stream, library
-
-
-def _same_device(ref, **tensors):
-    for name, t in tensors.items():
-        if t is not None and t.device != ref.device:
-            raise ValueError(f"{name} is on {t.device}, q on {ref.device}: one device only")
+from ._args import address, expect, on_device, stream
+from .wkv7 import ALGO, OK, WKV7Error, _check, _dtype_code, _head_norm, library
 
 
 def _sizes(q, k, v, g, s0, mask, cu_seqlens, head_first):
@@ -34,24 +29,24 @@ def _sizes(q, k, v, g, s0, mask, cu_seqlens, head_first):
     if v.dim() != 4:
         raise ValueError(f"v must have 4 dimensions, got {tuple(v.shape)}")
     V = v.shape[-1]
-    _check(k, "k", q.dtype, q.shape)
-    _check(v, "v", q.dtype, (*q.shape[:3], V))
+    expect(k, "k", q.dtype, q.shape, q)
+    expect(v, "v", q.dtype, (*q.shape[:3], V), q)
     _check(g, "g", q.dtype)
     per_head = g.dim() == 1
-    _check(g, "g", q.dtype, (H,) if per_head else q.shape[:3])
+    expect(g, "g", q.dtype, (H,) if per_head else q.shape[:3], q)
     N = B
     if cu_seqlens is not None:
         _check(cu_seqlens, "cu_seqlens", torch.int32)
         if cu_seqlens.dim() != 1 or cu_seqlens.numel() < 1:
             raise ValueError("cu_seqlens must be [N + 1]")
+        expect(cu_seqlens, "cu_seqlens", torch.int32, cu_seqlens.shape, q)
         N = cu_seqlens.numel() - 1
     if s0 is not None:
-        _check(s0, "s0", torch.float32, (N, H, K, V))
+        expect(s0, "s0", torch.float32, (N, H, K, V), q)
     if mask is not None:
         if mask.dtype == torch.bool:
             mask = mask.to(torch.uint8)
-        _check(mask, "mask", torch.uint8, (B, T))
-    _same_device(q, k=k, v=v, g=g, s0=s0, mask=mask, cu_seqlens=cu_seqlens)
+        expect(mask, "mask", torch.uint8, (B, T), q)
     return B, T, H, K, V, N, per_head, mask
 
 
@@ -59,7 +54,7 @@ def _workspace(given, nbytes, ref):
     if given is None:
         return torch.empty(nbytes, dtype=torch.uint8, device=ref.device) if nbytes else None
     _check(given, "workspace", torch.uint8)
-    _same_device(ref, workspace=given)
+    expect(given, "workspace", torch.uint8, given.shape, ref)
     return given
 
 
@@ -85,21 +80,20 @@ def wkv7_la_fwd(q, k, v, g, s0=None, mask=None, cu_seqlens=None, output_final_st
     if o is None:
         o = torch.empty_like(v)
     else:
-        _check(o, "o", q.dtype, v.shape)
+        expect(o, "o", q.dtype, v.shape, q)
     if output_final_state and sT is None:
         sT = torch.empty((N, H, K, V), dtype=torch.float32, device=q.device)
     elif sT is not None:
-        _check(sT, "sT", torch.float32, (N, H, K, V))
-    _same_device(q, o=o, sT=sT)
+        expect(sT, "sT", torch.float32, (N, H, K, V), q)
     lib = library()
-    with torch.cuda.device(q.device):
+    with on_device(q):
         need = int(lib.wkv7_la_fwd_workspace_bytes(B, T, H, K, V, N, int(cu_seqlens is not None),
                                                    _dtype_code(q), ALGO[algo]))
         ws = _workspace(workspace, need, q)
-        st = lib.wkv7_la_fwd(_ptr(q), _ptr(k), _ptr(v), _ptr(g), int(per_head), _ptr(s0),
-                             _ptr(mask), _ptr(o), _ptr(sT), B, T, H, K, V, _ptr(cu_seqlens), N,
+        st = lib.wkv7_la_fwd(address(q), address(k), address(v), address(g), int(per_head), address(s0),
+                             address(mask), address(o), address(sT), B, T, H, K, V, address(cu_seqlens), N,
                              float(scale), int(bool(head_first)), _dtype_code(q), ALGO[algo],
-                             _ptr(ws), 0 if ws is None else ws.numel(), _stream(q.device))
+                             address(ws), 0 if ws is None else ws.numel(), stream(q))
     if st != OK:
         raise WKV7Error(st, "wkv7_la_fwd")
     return o, sT
@@ -112,27 +106,24 @@ def wkv7_la_step(q, k, v, g, state, out_state=None, scale: float = 1.0, o=None):
     if q.dim() != 3:
         raise ValueError(f"q must have 3 dimensions, got {tuple(q.shape)}")
     B, H, K = q.shape
-    _check(v, "v", q.dtype)
     V = v.shape[-1]
-    _check(k, "k", q.dtype, (B, H, K))
-    _check(v, "v", q.dtype, (B, H, V))
-    _check(g, "g", q.dtype)
+    expect(k, "k", q.dtype, (B, H, K), q)
+    expect(v, "v", q.dtype, (B, H, V), q)
     per_head = g.dim() == 1
-    _check(g, "g", q.dtype, (H,) if per_head else (B, H))
-    _check(state, "state", torch.float32, (B, H, K, V))
+    expect(g, "g", q.dtype, (H,) if per_head else (B, H), q)
+    expect(state, "state", torch.float32, (B, H, K, V), q)
     if out_state is None:
         out_state = state
     else:
-        _check(out_state, "out_state", torch.float32, (B, H, K, V))
+        expect(out_state, "out_state", torch.float32, (B, H, K, V), q)
     if o is None:
         o = torch.empty_like(v)
     else:
-        _check(o, "o", q.dtype, (B, H, V))
-    _same_device(q, k=k, v=v, g=g, state=state, out_state=out_state, o=o)
-    with torch.cuda.device(q.device):
-        st = library().wkv7_la_step(_ptr(q), _ptr(k), _ptr(v), _ptr(g), int(per_head),
-                                    _ptr(state), _ptr(out_state), _ptr(o), B, H, K, V,
-                                    float(scale), _dtype_code(q), _stream(q.device))
+        expect(o, "o", q.dtype, (B, H, V), q)
+    with on_device(q):
+        st = library().wkv7_la_step(address(q), address(k), address(v), address(g), int(per_head),
+                                    address(state), address(out_state), address(o), B, H, K, V,
+                                    float(scale), _dtype_code(q), stream(q))
     if st != OK:
         raise WKV7Error(st, "wkv7_la_step")
     return o
@@ -145,12 +136,11 @@ def wkv7_la_bwd(q, k, v, g, dout, s0=None, mask=None, dsT=None, cu_seqlens=None,
     dg (input dtype, shaped like the inputs; dg of a [H] g is summed over batch and tokens) and
     ds0 (fp32 [N,H,K,V]); dg and ds0 are None when not needed."""
     B, T, H, K, V, N, per_head, mask = _sizes(q, k, v, g, s0, mask, cu_seqlens, head_first)
-    _check(dout, "dout", q.dtype, v.shape)
+    expect(dout, "dout", q.dtype, v.shape, q)
     if dsT is not None:
-        _check(dsT, "dsT", torch.float32, (N, H, K, V))
-    _same_device(q, dout=dout, dsT=dsT)
+        expect(dsT, "dsT", torch.float32, (N, H, K, V), q)
     lib = library()
-    with torch.cuda.device(q.device):
+    with on_device(q):
         need = int(lib.wkv7_la_bwd_workspace_bytes(B, T, H, K, V, N, int(cu_seqlens is not None),
                                                    _dtype_code(q), ALGO[algo]))
         ws = _workspace(workspace, need, q)
@@ -158,12 +148,12 @@ def wkv7_la_bwd(q, k, v, g, dout, s0=None, mask=None, dsT=None, cu_seqlens=None,
                "dg": torch.empty_like(g) if need_dg else None,
                "ds0": torch.empty((N, H, K, V), dtype=torch.float32, device=q.device)
                if need_ds0 else None}
-        st = lib.wkv7_la_bwd(_ptr(q), _ptr(k), _ptr(v), _ptr(g), int(per_head), _ptr(s0),
-                             _ptr(mask), _ptr(dout), _ptr(dsT), _ptr(out["dq"]), _ptr(out["dk"]),
-                             _ptr(out["dv"]), _ptr(out["dg"]), _ptr(out["ds0"]), B, T, H, K, V,
-                             _ptr(cu_seqlens), N, float(scale), int(bool(head_first)),
-                             _dtype_code(q), ALGO[algo], _ptr(ws),
-                             0 if ws is None else ws.numel(), _stream(q.device))
+        st = lib.wkv7_la_bwd(address(q), address(k), address(v), address(g), int(per_head), address(s0),
+                             address(mask), address(dout), address(dsT), address(out["dq"]), address(out["dk"]),
+                             address(out["dv"]), address(out["dg"]), address(out["ds0"]), B, T, H, K, V,
+                             address(cu_seqlens), N, float(scale), int(bool(head_first)),
+                             _dtype_code(q), ALGO[algo], address(ws),
+                             0 if ws is None else ws.numel(), stream(q))
     if st != OK:
         raise WKV7Error(st, "wkv7_la_bwd")
     return out

@@ -192,8 +192,8 @@ def test_step_refuses(clib, kw, status):
 
 def test_workspace_queries(clib):
     q = lib.wkv7_la_workspace_bytes
-    assert q(8, 4096, 64, dtype=F32) == 0          # units enough: nothing is cut
-    assert q(8, 4096, 64) > 0                      # states handed from block to block
+    assert q(8, 4096, 64) == 0                     # sequences fill the GPU: nothing is cut
+    assert q(5, 4096, 32) > 0                      # states handed from block to block
     assert q(1, 16384, 4) > 0 and q(1, 16384, 4, 128, 128) > q(1, 16384, 4)
     assert q(1, 100, 1) == 0 and q(1, 0, 1) == 0
     assert q(2, 100, 4, backward=True) > 0
