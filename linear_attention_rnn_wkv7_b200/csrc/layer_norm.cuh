@@ -91,6 +91,66 @@ template <int VEC> __device__ __forceinline__ void store(__nv_bfloat16* p, const
     }
 }
 
+// Pairs of fp32 in one instruction: per element the arithmetic of a row is then half, and HBM
+// and not the issue rate bounds the kernels (forward of 32768 x 4096 bf16: 193 us without).
+__device__ __forceinline__ uint64_t pair2(float a, float b) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ void split2(uint64_t x, float& a, float& b) {
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(x));
+}
+__device__ __forceinline__ float sum2(uint64_t x) {
+    float a, b;
+    split2(x, a, b);
+    return a + b;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+// A lone value (rows of odd lengths) goes through the same code.
+__device__ __forceinline__ float sum2(float x) { return x; }
+__device__ __forceinline__ float add2(float a, float b) { return a + b; }
+__device__ __forceinline__ float mul2(float a, float b) { return a * b; }
+__device__ __forceinline__ float fma2(float a, float b, float c) { return fmaf(a, b, c); }
+template <int VEC> struct PairOf { typedef uint64_t type; };
+template <> struct PairOf<1> { typedef float type; };
+template <int VEC> using Pair = typename PairOf<VEC>::type;
+template <int VEC> constexpr int pairs() { return VEC == 1 ? 1 : VEC / 2; }
+template <int VEC> __device__ __forceinline__ Pair<VEC> splat(float x) {
+    if constexpr (VEC == 1) return x;
+    else return pair2(x, x);
+}
+template <int VEC> __device__ __forceinline__ void to_pairs(const float (&v)[VEC], Pair<VEC> (&p)[pairs<VEC>()]) {
+    if constexpr (VEC == 1) {
+        p[0] = v[0];
+    } else {
+#pragma unroll
+        for (int q = 0; q < VEC / 2; ++q) p[q] = pair2(v[2 * q], v[2 * q + 1]);
+    }
+}
+template <int VEC> __device__ __forceinline__ void from_pairs(const Pair<VEC> (&p)[pairs<VEC>()], float (&v)[VEC]) {
+    if constexpr (VEC == 1) {
+        v[0] = p[0];
+    } else {
+#pragma unroll
+        for (int q = 0; q < VEC / 2; ++q) split2(p[q], v[2 * q], v[2 * q + 1]);
+    }
+}
+
 // VEC elements as they are in memory (prefetched rows), and as fp32.
 template <typename T, int VEC> struct Raw { T v[VEC]; };
 template <> struct Raw<__nv_bfloat16, 8> { uint4 v; };
@@ -215,7 +275,7 @@ template <int TPR> constexpr int block_threads() { return TPR <= 32 ? 128 : TPR;
 // Blocks per SM, by the registers that a row of N elements a thread, the next one, the weights and
 // (backward) the sums of dw and db take.
 template <int TPR, int N> constexpr int fwd_blocks() {
-    constexpr int threads = N <= 8 ? 1536 : N <= 16 ? 1024 : 512;
+    constexpr int threads = N <= 8 ? 1024 : N <= 16 ? 640 : 512;
     return threads / block_threads<TPR>() > 0 ? threads / block_threads<TPR>() : 1;
 }
 template <int TPR, int N> constexpr int bwd_blocks() {
@@ -230,7 +290,7 @@ __global__ void __launch_bounds__(block_threads<TPR>(), fwd_blocks<TPR, NI * VEC
 ln_fwd_kernel(const T* __restrict__ x, const Tw* __restrict__ w, const Tw* __restrict__ b,
               T* __restrict__ y, float* __restrict__ mean, float* __restrict__ rstd, Shape s) {
     __shared__ float red[2][2][32];
-    constexpr int kTeams = block_threads<TPR>() / TPR;
+    constexpr int kTeams = block_threads<TPR>() / TPR, P = pairs<VEC>();
     const int lane = threadIdx.x % TPR;
     const long long team = (long long)blockIdx.x * kTeams + threadIdx.x / TPR;
     const bool in = team < s.teams;
@@ -268,48 +328,67 @@ ln_fwd_kernel(const T* __restrict__ x, const Tw* __restrict__ w, const Tw* __res
     long long k = first;
     for (long long turn = 0; turn < turns; ++turn, k += step) {
         const bool ok = in && k < per;
-        float xr[NI][VEC], m = 0.f, m2 = 0.f;
+        Pair<VEC> xr[NI][P], sum = 0;
+        float m, m2;
 #pragma unroll
         for (int i = 0; i < NI; ++i) {
             const bool live = ok && (i * TPR + lane) * VEC < s.D;
+            float v[VEC];
             if (live) {
-                unpack<VEC>(next[i], xr[i]);
+                unpack<VEC>(next[i], v);
             } else {
 #pragma unroll
-                for (int q = 0; q < VEC; ++q) xr[i][q] = 0.f;
+                for (int q = 0; q < VEC; ++q) v[q] = 0.f;
             }
+            to_pairs<VEC>(v, xr[i]);
 #pragma unroll
-            for (int q = 0; q < VEC; ++q) m += xr[i][q];
+            for (int q = 0; q < P; ++q) sum = add2(sum, xr[i][q]);
         }
         fetch(k + step);
-        m *= inv_n;
+        m = sum2(sum) * inv_n;
+        const Pair<VEC> mm = splat<VEC>(-m);
+        sum = 0;
 #pragma unroll
         for (int i = 0; i < NI; ++i) {
             if ((i * TPR + lane) * VEC < s.D) {
 #pragma unroll
-                for (int q = 0; q < VEC; ++q) m2 = fmaf(xr[i][q] - m, xr[i][q] - m, m2);
+                for (int q = 0; q < P; ++q) {
+                    const Pair<VEC> d = add2(xr[i][q], mm);
+                    sum = fma2(d, d, sum);
+                }
             }
         }
+        m2 = sum2(sum);
         merge(m, m2, red[turn & 1]);
         const float r = 1.f / sqrtf(m2 * inv_d + s.eps);
         if (ok) {
             const long long row = row_at(s, k, group);
             T* py = y + row * s.D;
+            const Pair<VEC> rr = splat<VEC>(r), minus = splat<VEC>(-m);
 #pragma unroll
             for (int i = 0; i < NI; ++i) {
                 const int e = (i * TPR + lane) * VEC;
                 if (e < s.D) {
-                    float wv[VEC], bv[VEC];
-                    if (w) unpack<VEC>(wr[i], wv);
-                    if (b) unpack<VEC>(br[i], bv);
-#pragma unroll
-                    for (int q = 0; q < VEC; ++q) {
-                        float v = (xr[i][q] - m) * r;
-                        if (w) v *= wv[q];
-                        if (b) v += bv[q];
-                        xr[i][q] = v;
+                    Pair<VEC> wp[P], bp[P];
+                    float v[VEC];
+                    if (w) {
+                        unpack<VEC>(wr[i], v);
+                        to_pairs<VEC>(v, wp);
                     }
-                    store<VEC>(py + e, xr[i]);
+                    if (b) {
+                        unpack<VEC>(br[i], v);
+                        to_pairs<VEC>(v, bp);
+                    }
+#pragma unroll
+                    for (int q = 0; q < P; ++q) {
+                        Pair<VEC> t = mul2(add2(xr[i][q], minus), rr);
+                        if (w && b) t = fma2(t, wp[q], bp[q]);
+                        else if (w) t = mul2(t, wp[q]);
+                        else if (b) t = add2(t, bp[q]);
+                        xr[i][q] = t;
+                    }
+                    from_pairs<VEC>(xr[i], v);
+                    store<VEC>(py + e, v);
                 }
             }
             if (lane == 0) {
@@ -340,11 +419,12 @@ ln_bwd_kernel(const T* __restrict__ x, const T* __restrict__ dy, const float* __
     const long long first = in ? team / s.G : 0;
     const long long turns = (per - (long long)blockIdx.x * kTeams / s.G + step - 1) / step;
     const long long wo = (long long)group * s.D;
-    float dw[kParam ? NI : 1][VEC], db[kParam ? NI : 1][VEC];
+    constexpr int P = pairs<VEC>();
+    Pair<VEC> dwp[kParam ? NI : 1][P], dbp[kParam ? NI : 1][P];
 #pragma unroll
     for (int i = 0; i < (kParam ? NI : 1); ++i)
 #pragma unroll
-        for (int q = 0; q < VEC; ++q) dw[i][q] = db[i][q] = 0.f;
+        for (int q = 0; q < P; ++q) dwp[i][q] = dbp[i][q] = 0;
     Raw<Tw, VEC> wr[NI];
     Raw<T, VEC> nx[NI], nd[NI];
     float nm = 0.f, nr = 0.f;
@@ -373,49 +453,66 @@ ln_bwd_kernel(const T* __restrict__ x, const T* __restrict__ dy, const float* __
         const bool ok = in && k < per;
         if (!kPrefetch) fetch(k);
         const float m = nm, r = nr;
-        float xh[NI][VEC], u[NI][VEC];
-        float a[2] = {0.f, 0.f};
+        Pair<VEC> xh[NI][P], u[NI][P], s0 = 0, s1 = 0;
 #pragma unroll
         for (int i = 0; i < NI; ++i) {
             if (ok && (i * TPR + lane) * VEC < s.D) {
-                unpack<VEC>(nx[i], xh[i]);
-                unpack<VEC>(nd[i], u[i]);
+                float v[VEC];
+                unpack<VEC>(nx[i], v);
+                to_pairs<VEC>(v, xh[i]);
+                unpack<VEC>(nd[i], v);
+                to_pairs<VEC>(v, u[i]);
             }
         }
         if (kPrefetch) fetch(k + step);
+        const Pair<VEC> rr = splat<VEC>(r), minus = splat<VEC>(-m);
 #pragma unroll
         for (int i = 0; i < NI; ++i) {
             if (ok && (i * TPR + lane) * VEC < s.D) {
-                float wv[VEC];
+                Pair<VEC> wp[P];
                 if (w && !kPrefetch) wr[i] = load_raw<Tw, VEC>(w + wo + (i * TPR + lane) * VEC);
-                if (w) unpack<VEC>(wr[i], wv);
+                if (w) {
+                    float v[VEC];
+                    unpack<VEC>(wr[i], v);
+                    to_pairs<VEC>(v, wp);
+                }
 #pragma unroll
-                for (int q = 0; q < VEC; ++q) {
-                    xh[i][q] = (xh[i][q] - m) * r;
+                for (int q = 0; q < P; ++q) {
+                    xh[i][q] = mul2(add2(xh[i][q], minus), rr);
                     if (kParam) {
-                        dw[i][q] = fmaf(u[i][q], xh[i][q], dw[i][q]);
-                        db[i][q] += u[i][q];
+                        dwp[i][q] = fma2(u[i][q], xh[i][q], dwp[i][q]);
+                        dbp[i][q] = add2(dbp[i][q], u[i][q]);
                     }
-                    if (w) u[i][q] *= wv[q];
-                    a[0] += u[i][q];
-                    a[1] = fmaf(u[i][q], xh[i][q], a[1]);
+                    if (w) u[i][q] = mul2(u[i][q], wp[q]);
+                    s0 = add2(s0, u[i][q]);
+                    s1 = fma2(u[i][q], xh[i][q], s1);
                 }
             }
         }
+        float a[2] = {sum2(s0), sum2(s1)};
         team_sum<TPR, 2>(a, red[turn & 1]);
-        const float c0 = a[0] * inv, c1 = a[1] * inv;
+        const Pair<VEC> c0 = splat<VEC>(-a[0] * inv), c1 = splat<VEC>(-a[1] * inv);
         if (ok) {
             T* pd = dx + row_at(s, k, group) * s.D;
 #pragma unroll
             for (int i = 0; i < NI; ++i) {
                 const int e = (i * TPR + lane) * VEC;
                 if (e < s.D) {
+                    float v[VEC];
 #pragma unroll
-                    for (int q = 0; q < VEC; ++q) xh[i][q] = r * (u[i][q] - c0 - xh[i][q] * c1);
-                    store<VEC>(pd + e, xh[i]);
+                    for (int q = 0; q < P; ++q)
+                        xh[i][q] = mul2(rr, fma2(xh[i][q], c1, add2(u[i][q], c0)));
+                    from_pairs<VEC>(xh[i], v);
+                    store<VEC>(pd + e, v);
                 }
             }
         }
+    }
+    float dw[kParam ? NI : 1][VEC], db[kParam ? NI : 1][VEC];
+#pragma unroll
+    for (int i = 0; i < (kParam ? NI : 1); ++i) {
+        from_pairs<VEC>(dwp[i], dw[i]);
+        from_pairs<VEC>(dbp[i], db[i]);
     }
     if constexpr (kParam && kBlockSum) {
         // the block's teams, in order, through shared memory
