@@ -9,33 +9,43 @@
 //     P  = X Y^T   (128 x 128, contraction D)      then E, the mask and the scale -> bf16
 //     Oi = P Z     (128 x D, contraction 128)      P read from tensor memory
 //     Ox = X U0    (128 x D, contraction D)        U0 rounded to bf16
-//     dU = (k . Y)^T Z   (D x D, contraction 128, twice: k . Y in two bf16 parts)
+//     dU = (k . Y)^T Z   (D x D, contraction 128, once for each bf16 part of k . Y)
 // Every exponent is a difference over a stretch of tokens, so decays of any strength are
 // exact (nothing is divided by a small prefix).  X, Y, Z enter raw, as TMA left them.
 //
 // Roundings to bf16: P (as the scores of any attention) and the copy of U0 that Ox reads, each a half
-// step of bf16 of one of the two parts of out.  The state itself is fp32 in registers, and its
-// update's operand is split in two bf16 parts (16 bits), so states and their gradients are as
-// good as fp32's: one bf16 part left the final state 2e-3 off, and two cost one more product
-// on a tensor pipe that is half idle.
+// step of bf16 of one of the two terms of out.  The state itself is fp32 in registers, and where it
+// is a result (a final state, dS0, a segment's start) its update's operand is split in three
+// bf16 parts (24 bits), so that it is as good as fp32's: with one part it was 2e-3 off, with two
+// 2.5e-6.  Where it only makes bf16 results two parts do.
 //
-// Bound: 4 tiles of 128 x D bf16 per chunk and SM from and to HBM (1500 ns at D = 64,
-// 3000 ns at D = 128 for a GPU's even share) against about 1200 and 2600 cycles of MMA,
-// so the kernel is built to keep loads in flight.  One persistent CTA of 16 warps per SM, each with
-// one job, so that a chunk's dependent steps overlap with other chunks':
-//     warp 0       TMA loads of X, Y, Z into a ring of stages (4 at D = 64, 2 at D = 128)
+// What bounds it.  At D = 64 a chunk moves 64 KB from and to HBM (1.5 us at an SM's even share)
+// and takes about 1400 cycles of MMA; it takes 2.1 to 2.4 us, because the roles of a chunk
+// (below) each run on one warp per scheduler, at a third of its issue rate: latencies of
+// tensor memory, shared memory and barriers, and instruction fetch (see wait_slow).  At D = 128
+// it takes 4.1 us against 3 us.
+// B = 8, T = 4096, H = 64 of 64: 336 us, 3.3 TB/s, half of the measured copy rate (fp32
+// recurrence 3480 us); 16384 tokens of 16 heads of 128: 142 us with its states made beforehand.
+// Tried and left: output staged in a tile of its own (the smaller ring cost as much); rows
+// of the decay scan on all lanes (slower: longer shuffles); waits as calls (each cost the MMA
+// warp 200 cycles more); score blocks of 32 columns (faster alone, slower with all SMs at it).
+//
+// One persistent CTA of 16 warps per SM, each with one job, so that a chunk's dependent steps
+// overlap with other chunks':
+//     warp 0       TMA loads of X, Y, Z into a ring of stages (3 at D = 64, 2 at D = 128)
 //     warp 1       issues all MMAs
-//     warp 2       decays: prefix sums (64-bit), factors; clears Z's unused rows
-//     warp 3       output tiles shared -> HBM, frees the stage
-//     warps 4-7    P: scores -> E . scores in bf16, in place in tensor memory
+//     warp 2       decays: prefix sums, factors; clears Z's unused rows
+//     warp 3       output tiles shared -> HBM, frees the stage's Z
+//     warps 4-7    P: scores -> E . scores in bf16, in place in tensor memory;
+//                  at D = 128 also half of k . Y
 //     warps 8-11   half of k . Y in parts; the state (at D = 128 half its columns)
-//     warps 12-15  out = f . Ox + Oi; at D = 64 the other half of k . Y, at D = 128 (where
-//                  warps 4-7 make that) the other half of the state
-// The chain from one chunk to the next is only U0 -> bf16 -> (Ox, dU) -> U1; the state never
-// goes through tensor memory.  All waits are on mbarriers and bounded (a second); a thread that
-// gives up sets a flag that ends every other wait, so the CTA always reaches its end, waits
-// for its copies and MMAs in flight (bounded), frees its tensor memory and reports
-// WKV7_ERR_DEVICE_TIMEOUT.
+//     warps 12-15  out = f . Ox + Oi; at D = 64 the other half of k . Y, at D = 128 the other
+//                  half of the state
+// The chain from one chunk to the next is only U0 -> bf16 -> Ox and (D = 128) dU -> U1; the state
+// never goes through tensor memory.  All waits are on mbarriers (or a flag in global memory)
+// and bounded; a thread that gives up sets a flag that ends every other wait, so the CTA
+// always reaches its end, waits for its copies and MMAs in flight (bounded), frees its tensor
+// memory and reports WKV7_ERR_DEVICE_TIMEOUT.
 #pragma once
 #include <cuda.h>
 
@@ -201,8 +211,9 @@ enum Bar {
 // The slow path of a wait, out of line: the roles' code has to fit the SM's instruction cache
 // together (as unrolled as each role alone would like it did not, and with all SMs at it
 // every role ran at the pace of instruction fetches from the level behind, half as fast).
-// Polls for at most a second, or until another thread has given up.
-__device__ __noinline__ bool wait_slow(uint32_t bar, uint32_t parity, volatile int* abort) {
+// Polls for at most `limit` ns, or until another thread has given up.
+__device__ __noinline__ bool wait_slow(uint32_t bar, uint32_t parity, volatile int* abort,
+                                       uint64_t limit) {
     uint64_t t0 = 0;
     for (uint32_t k = 0; k < (1u << 28); ++k) {
         if (mbar_try_wait(bar, parity)) return true;
@@ -210,7 +221,7 @@ __device__ __noinline__ bool wait_slow(uint32_t bar, uint32_t parity, volatile i
             if (*abort) return false;
             const uint64_t now = globaltimer_ns();
             if (t0 == 0) t0 = now;
-            if (now - t0 > 1000000000ull) break;
+            if (now - t0 > limit) break;
         }
     }
     *abort = 1;
@@ -218,14 +229,14 @@ __device__ __noinline__ bool wait_slow(uint32_t bar, uint32_t parity, volatile i
     return false;
 }
 
-__device__ __noinline__ bool handoff_slow(const unsigned* flag, volatile int* abort) {
+__device__ __noinline__ bool handoff_slow(const unsigned* flag, volatile int* abort, uint64_t limit) {
     const uint64_t t0 = globaltimer_ns();
     for (uint32_t k = 0; k < (1u << 28); ++k) {
         unsigned v;
         asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(flag) : "memory");
         if (v != 0) return true;
         if (*abort) return false;
-        if (globaltimer_ns() - t0 > 1000000000ull) break;
+        if (globaltimer_ns() - t0 > limit) break;
         __nanosleep(100);
     }
     *abort = 1;
@@ -236,10 +247,11 @@ __device__ __noinline__ bool handoff_slow(const unsigned* flag, volatile int* ab
 struct Ctx {
     uint32_t sbase, bars;
     volatile int* abort;
+    uint64_t limit;  // of a wait, in ns
     __device__ __forceinline__ uint32_t bar(int i) const { return bars + 8 * i; }
     // A bounded wait; false: give up (every role then leaves its loop).
     __device__ __forceinline__ bool wait(int i, uint32_t parity) const {
-        return mbar_try_wait(bar(i), parity) || wait_slow(bar(i), parity, abort);
+        return mbar_try_wait(bar(i), parity) || wait_slow(bar(i), parity, abort, limit);
     }
     // The same for a whole warp: all lanes go on, or none (what follows is warp-wide).
     __device__ __forceinline__ bool wait_warp(int i, uint32_t parity) const {
@@ -248,7 +260,7 @@ struct Ctx {
     __device__ __forceinline__ void arrive(int i) const { mbar_arrive(bar(i)); }
     // The flag of a state handed on, for a whole warp (bounded as the other waits).
     __device__ __forceinline__ bool wait_handoff(const unsigned* flag) const {
-        return __all_sync(0xffffffffu, handoff_slow(flag, abort));
+        return __all_sync(0xffffffffu, handoff_slow(flag, abort, limit));
     }
 };
 
@@ -457,6 +469,9 @@ la_chunked_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constan
     Ctx cx;
     cx.sbase = smem_u32(smem);
     cx.bars = cx.sbase + C::OFF_BAR;
+    // A second; and for a sequence longer than a run, the CTAs before this one work on it in turn
+    // first (20 us for each of their chunks, several times what one takes).
+    cx.limit = 1000000000ull + 20000ull * (uint64_t)p.run * blockIdx.x;
     cx.abort = reinterpret_cast<volatile int*>(smem + C::OFF_BAR + 8 * kBars);
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::OFF_BAR + 8 * kBars + 4);
     if (cx.sbase & 1023u) {  // the swizzled tiles need a 1024-byte aligned base

@@ -31,7 +31,8 @@
 namespace wkv7 {
 namespace la {
 
-// Tokens per chunk of the tensor-core kernel; segments are multiples of it.
+// Tokens per chunk of the tensor-core kernel; its segments are multiples of it, the recurrent
+// kernel's of kRecChunk.
 constexpr int kChunk = 128;
 // Spacing of the states that the recurrent kernel keeps for dg: fp32 results want shorter
 // sums than bf16's (summed over the tokens of 900, with memories of 3 to 30 tokens, dg was
@@ -139,11 +140,11 @@ struct Pass {
     float inter_scale;    // on what the state before the chunk gives to out
     float key_scale;      // on y_t z_t^T inside the state
     int parts;            // bf16 parts of the state update's operand (tensor cores): 3 where the
-                          // state itself is a result, 1 where it only makes bf16 results
+                          // state itself is a result, 2 where it only makes bf16 results
     int run;              // > 0: chunks per block, see Schedule (tensor-core kernel); else segments
     float* ho_state;      // [block][D * D], and
     unsigned* ho_flag;    // [block][8], zero: states handed from block to block
-    int seg;              // tokens per segment (a multiple of kChunk)
+    int seg;              // tokens per segment
     const float* init;    // states before the first token: [N][H][D][D], or by slot when
     int init_by_slot;     // init_by_slot; nullptr: zeros
     int init_transposed;  // init holds [z][y] instead of [y][z]

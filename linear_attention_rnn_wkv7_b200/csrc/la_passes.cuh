@@ -26,10 +26,12 @@ struct Problem {
 // How the work is laid out on the GPU.  One segment per sequence needs nothing extra.  With fewer
 // (sequence, head) units than the GPU holds blocks, sequences are cut: a pass over y and z first
 // gives every segment's own state (half of a pass's reads, no outputs), la_chain_kernel
-// joins them, and all segments run at once.  The estimate counts chunks of time on the longest
-// block: a segment costs about two more than its chunks (its state's way in and out), a state-only pass
-// 0.6 of a full one, the join a third per segment, the launches four.  With at least as many
-// units as blocks the tensor-core kernel takes runs (la_chunked.cuh, Schedule) instead.
+// joins them, and all segments run at once.  The estimate counts time on the longest block in
+// grains, 128 tokens for the tensor-core kernel (2 to 4 us) and 32 for the recurrent one (about
+// 10 us): a segment costs its grains and its state's way in and out, a state-only pass 0.6 of a
+// full one, the join and the launches the rest (16384 tokens x 16 heads of 128: 64 segments
+// 414 us, the 9 that this picks 144 us; fp32 333 tokens x 16 units: uncut 115 us).  With more
+// units than blocks the tensor-core kernel takes runs (la_chunked.cuh, Schedule) instead.
 struct Plan {
     int seg;
     bool split;
@@ -42,9 +44,13 @@ inline Plan make_plan(const Problem& p) {
     const Geom& g = p.geom;
     // blocks that run at once: one per SM (tensor cores) or by registers (64 a state tile)
     const long long resident = p.chunked ? kBlocks : (long long)kBlocks * 384 / p.D;
-    const long long chunks = std::max<long long>(1, ((long long)g.T + kChunk - 1) / kChunk);
-    Plan best{(int)(chunks * kChunk), false, 0, 0};
-    if ((long long)chunks * kChunk > 0x7fffff80LL) best.seg = 0x7fffff80;
+    // segments are whole grains; costs in grains of time
+    const int grain = p.chunked ? kChunk : kRecChunk;
+    const double per_segment = p.chunked ? 2.0 : 0.3, launches = p.chunked ? 4.0 : 0.6,
+                 join = p.chunked ? 0.35 : 0.05;
+    const long long chunks = std::max<long long>(1, ((long long)g.T + grain - 1) / grain);
+    Plan best{(int)(chunks * grain), false, 0, 0};
+    if (chunks * grain > 0x7fffff80LL) best.seg = 0x7fffff80;
     const long long units = (long long)g.N * g.H * p.slabs();
     const long long all = g.slots(kChunk) * g.H;
     // Whole sequences round robin keep neighbouring heads, whose rows share DRAM pages, at work
@@ -58,22 +64,22 @@ inline Plan make_plan(const Problem& p) {
         best.blocks = (all + best.run - 1) / best.run;
         return best;
     }
-    if (chunks < 4) return best;
+    if (chunks < 4 || units == 0) return best;
     if (g.cu) {
         // lengths are on the device: cut only sequences longer than an even share
         const long long share = chunks * g.H * p.slabs() / resident;
         const long long c = std::max<long long>(4, share);
-        if (c < chunks) best = Plan{(int)(c * kChunk), true, 0, 0};
+        if (c < chunks) best = Plan{(int)(c * grain), true, 0, 0};
         return best;
     }
-    double least = (double)((units + resident - 1) / resident) * (double)(chunks + 2);
+    double least = (double)((units + resident - 1) / resident) * ((double)chunks + per_segment);
     for (long long n = 2; n <= std::min<long long>(chunks, 256); ++n) {
         const long long c = (chunks + n - 1) / n, used = (chunks + c - 1) / c;
         const double waves = (double)((units * used + resident - 1) / resident);
-        const double t = waves * (double)(c + 2) + waves * (0.6 * (double)c + 2) + 0.35 * (double)used + 4;
+        const double t = waves * (1.6 * (double)c + 2 * per_segment) + join * (double)used + launches;
         if (used > 1 && t < least) {
             least = t;
-            best = Plan{(int)(c * kChunk), true, 0, 0};
+            best = Plan{(int)(c * grain), true, 0, 0};
         }
     }
     return best;
@@ -190,7 +196,7 @@ inline cudaError_t forward(const Problem& p, const Tin* q, const Tin* k, const T
     a.out = o;
     a.pair_scale = a.inter_scale = scale;
     a.key_scale = 1.f;
-    a.parts = sT || plan.split ? 3 : 1;
+    a.parts = sT || plan.split ? 3 : 2;
     a.seg = plan.seg;
     a.init = s0;
     a.fin = sT;
@@ -222,13 +228,14 @@ inline cudaError_t backward(const Problem& p, const Tin* q, const Tin* k, const 
     f.g = g;
     f.g_per_head = g_per_head;
     f.mask = mask;
-    // dq's kept states meet sums of their own terms in dg, whose difference counts
-    f.parts = plan.split ? 3 : dg ? 2 : 1;
+    // (one part would add as much error to dq, dk and dg as all other roundings: 3.6e-3 in dk of
+    // a padded batch, two 2.3e-3)
+    f.parts = plan.split ? 3 : 2;
     f.seg = plan.seg;
     Pass<Tin> r = f;  // against it
     r.pair_scale = r.key_scale = scale;
     r.inter_scale = 1.f;
-    r.parts = ds0 || plan.split ? 3 : 1;
+    r.parts = ds0 || plan.split ? 3 : 2;
     f.pair_scale = f.inter_scale = scale;
     f.key_scale = 1.f;
     f.init = s0;
@@ -281,7 +288,7 @@ inline cudaError_t backward(const Problem& p, const Tin* q, const Tin* k, const 
     a.x = v;
     a.y = dout;
     a.z = q;
-    a.parts = 1;  // its state is no result
+    a.parts = 2;  // its state is no result
     a.out = dk;
     a.init_transposed = 1;
     if (dg) {
