@@ -117,6 +117,9 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
     const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
     return *reinterpret_cast<const uint32_t*>(&h);
 }
+__device__ __forceinline__ void prefetch_l2(const void* p) {
+    asm volatile("prefetch.global.L2 [%0];" ::"l"(p));
+}
 __device__ __forceinline__ void st_shared16(uint32_t addr, uint32_t a, uint32_t b, uint32_t c,
                                             uint32_t d) {
     asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c),
@@ -1060,6 +1063,31 @@ la_chunked_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constan
                     rowf = p.inter_scale * ex2(kRev ? sc->c[127] - sc->c[row] : sc->c[row]);
                     row_out = (sc->out[w] >> lane) & 1;
                 }
+                // What comes from HBM for dg, the chunk's kept state and the rows of out's dot
+                // products, is on its way to L2 a chunk ahead (in registers it would have to
+                // live across the work below, and did not fit).
+                if constexpr (kGrad) {
+                    if (i + 1 < wk.chunks) {
+                        const int t1 = wk.first_token(i + 1);
+                        if (kRev && has_state) {
+                            const float* ck = static_cast<const float*>(p.ck) +
+                                              wk.unit(G, t1) * (D * D) + (sthread >> 3) * 32;
+                            // 32 floats a line: lines (thread / 8), + kSThreads / 8, ..
+                            if ((sthread & 7) == 0) {
+#pragma unroll
+                                for (int l = 0; l < R / 4; ++l)
+                                    prefetch_l2(ck + l * kSThreads * 4);
+                            }
+                        }
+                        const int t = t1 + 32 * w + lane;
+                        if (!first && t < wk.te) {
+                            const __nv_bfloat16* src =
+                                p.dot_with + (rw.first + (long long)t * rw.step) * D;
+#pragma unroll
+                            for (int l = 0; l < D / 64; ++l) prefetch_l2(src + 64 * l);
+                        }
+                    }
+                }
                 // k . Y: of the next chunk where there is room for two (half of it here, half
                 // there), of this one with warps 4-7 otherwise
                 if (C::kAhead) {
@@ -1074,6 +1102,18 @@ la_chunked_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constan
                 }
                 if (!ok) break;
 
+                constexpr bool kRowAhead = kGrad && !first && D == 64;
+                uint4 wrow[kRowAhead ? D / 8 : 1];
+                if constexpr (kRowAhead) {
+                    const int t = t0 + 32 * w + lane;
+                    if (t < wk.te && row_out) {
+                        const uint4* src = reinterpret_cast<const uint4*>(
+                            p.dot_with + (rw.first + (long long)t * rw.step) * D);
+#pragma unroll
+                        for (int u = 0; u < D / 8; ++u) wrow[u] = src[u];
+                    }
+                }
+
                 // Backward in time: <S_end, G_end> of the chunk, with G_end rounded as the
                 // product X U0 reads it.  What tokens s >= t take from it in dL/dc is then
                 // the same sum's own terms, and the difference, e^{c_L - c_t} <S_t, G_end>,
@@ -1082,10 +1122,13 @@ la_chunked_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constan
                 if (kGrad && kRev && has_state) {
                     const long long u = wk.unit(G, t0);
                     const float4* ck = static_cast<const float4*>(p.ck) + u * (D * D / 4) + sthread;
+                    float4 kept[R / 4];
+#pragma unroll
+                    for (int q = 0; q < R / 4; ++q) kept[q] = ck[q * kSThreads];
                     float s = 0.f;
 #pragma unroll
                     for (int q = 0; q < R / 4; ++q) {
-                        const float4 v = ck[q * kSThreads];
+                        const float4 v = kept[q];
                         const uint32_t a = pack_bf16(S[4 * q], S[4 * q + 1]);
                         const uint32_t b = pack_bf16(S[4 * q + 2], S[4 * q + 3]);
                         s = fmaf(v.x, __uint_as_float(a << 16), s);
@@ -1158,7 +1201,13 @@ la_chunked_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constan
                         tmem_ld16(to + C::TM_OX + q, ox);
                         tmem_ld16(to + C::TM_OI + q, oi);
                         uint4 wv[V / 8];
-                        if (kGrad && in && row_out) {
+                        if constexpr (kRowAhead) {
+                            // (rolled: the row's registers are picked by the turn)
+#pragma unroll
+                            for (int u = 0; u < V / 8; ++u)
+                                wv[u] = q == 0 ? wrow[u] : q == 16 ? wrow[2 + u]
+                                        : q == 32 ? wrow[4 + u] : wrow[6 + u];
+                        } else if (kGrad && in && row_out) {
                             const uint4* src =
                                 reinterpret_cast<const uint4*>(p.dot_with + grow * D + q);
 #pragma unroll
@@ -1196,7 +1245,7 @@ la_chunked_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constan
                     }
                     tc_fence_before();
                     cx.arrive(kOFree);
-                    if (kGrad && in) p.dots[grow] = dot;
+                    if (kGrad && in) p.dots[scratch_of(G, wk.it, wk.h, t)] = dot;
                     fence_proxy_async();
                     cx.arrive(kStore + at_.st);
                 }

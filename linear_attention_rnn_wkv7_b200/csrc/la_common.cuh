@@ -125,6 +125,12 @@ __device__ __forceinline__ Rows rows_of(const Geom& g, const Item& it, int h) {
     return r;
 }
 
+// Index of token t of head h in scratch values of one per token and head: head first whatever
+// the layout, so that a chunk's are contiguous.
+__device__ __forceinline__ long long scratch_of(const Geom& g, const Item& it, int h, int t) {
+    return ((long long)it.bb * g.H + h) * g.T + it.bos + t;
+}
+
 // One pass: out = A(x, y, z) or A'(x, y, z).
 template <typename Tin>
 struct Pass {
@@ -153,8 +159,8 @@ struct Pass {
     float* seg_state;     // [slot][H][D][D]
     float* seg_decay;     // [slot][H]
     // gradient of the log decays
-    const Tin* dot_with;  // dots[row] = dot_with[row] . out[row] before rounding
-    float* dots;          // [slab][rows]
+    const Tin* dot_with;  // dots = dot_with[row] . out[row] before rounding, one for each
+    float* dots;          // [slab][B][H][T]
     long long dots_stride;
     void* ck;             // states at each chunk's end (layout private to the kernel)
     float* ck_dot;        // [chunk slot][H][parts]: parts of <ck, state before the chunk>
@@ -244,8 +250,8 @@ la_dg_kernel(Geom g, const uint8_t* __restrict__ mask, const float* __restrict__
         v[i] = 0.f;
         live[i] = t < it.len;
         if (live[i]) {
-            const long long row = rw.first + t * rw.step;
-            for (int s = 0; s < slabs; ++s) v[i] += qdq[s * stride + row] - kdk[s * stride + row];
+            const long long at = scratch_of(g, it, h, t);
+            for (int s = 0; s < slabs; ++s) v[i] += qdq[s * stride + at] - kdk[s * stride + at];
             if (mask) live[i] = mask[(long long)it.bb * g.T + it.bos + t] != 0;
         }
     }

@@ -302,7 +302,8 @@ la_recurrent_kernel(const Pass<Tin> p) {
                     }
 #pragma unroll
                     for (int m = 16; m > 0; m >>= 1) s += __shfl_xor_sync(0xffffffffu, s, m);
-                    if (lane == 0) p.dots[slab * p.dots_stride + row] = s;
+                    if (lane == 0)
+                        p.dots[slab * p.dots_stride + scratch_of(G, it, h, token(cur, i))] = s;
                 }
                 p.out[at] = from_f32<Tin>(o.x);
                 p.out[at + 1] = from_f32<Tin>(o.y);
