@@ -451,7 +451,9 @@ wkv7_status wkv7_la_step(const void* q, const void* k, const void* v, const void
  *                                        order), or NULL to skip
  *   ds0            [N, H, K, V]  fp32    or NULL to skip; must not alias s0 or dsT
  *   workspace      at least wkv7_la_bwd_workspace_bytes(..) bytes, 16-byte aligned; calls
- *                  that may overlap need workspaces of their own
+ *                  that may overlap need workspaces of their own.  Mostly states kept for
+ *                  dg, every 128 tokens (tensor cores) or 32 (recurrent): 136 or 520 bytes
+ *                  per token and head at head size 64
  *
  * The results do not depend on scheduling (no atomic sums).
  */

@@ -275,7 +275,7 @@ template <int TPR> constexpr int block_threads() { return TPR <= 32 ? 128 : TPR;
 // Blocks per SM, by the registers that a row of N elements a thread, the next one, the weights and
 // (backward) the sums of dw and db take.
 template <int TPR, int N> constexpr int fwd_blocks() {
-    constexpr int threads = N <= 8 ? 1024 : N <= 16 ? 640 : 512;
+    constexpr int threads = N <= 16 ? 640 : 512;
     return threads / block_threads<TPR>() > 0 ? threads / block_threads<TPR>() : 1;
 }
 template <int TPR, int N> constexpr int bwd_blocks() {
@@ -291,6 +291,12 @@ ln_fwd_kernel(const T* __restrict__ x, const Tw* __restrict__ w, const Tw* __res
               T* __restrict__ y, float* __restrict__ mean, float* __restrict__ rstd, Shape s) {
     __shared__ float red[2][2][32];
     constexpr int kTeams = block_threads<TPR>() / TPR, P = pairs<VEC>();
+    // 1024 threads have 64 registers each: long rows leave none for the weights, which come
+    // from L1 each row then (32768 x 4096 bf16 with fp32 weights: held 134 us, not held 177 us).
+    constexpr bool kHold = TPR < 1024 || NI * VEC <= 8;
+    // Rows on their way: short rows leave registers for three (262144 x 64: 31 us with one, 23
+    // with three), longer ones do not (32768 x 4096: 134 us with one, 146 with three)
+    constexpr int kDepth = TPR < 1024 && NI * VEC <= 8 ? 3 : 1;
     const int lane = threadIdx.x % TPR;
     const long long team = (long long)blockIdx.x * kTeams + threadIdx.x / TPR;
     const bool in = team < s.teams;
@@ -302,18 +308,18 @@ ln_fwd_kernel(const T* __restrict__ x, const Tw* __restrict__ w, const Tw* __res
     const long long turns = (per - (long long)blockIdx.x * kTeams / s.G + step - 1) / step;
     const long long wo = (long long)group * s.D;
     float count = 0.f;
-    Raw<T, VEC> next[NI];
+    Raw<T, VEC> next[kDepth][NI];
     Raw<Tw, VEC> wr[NI], br[NI];
 #pragma unroll
     for (int i = 0; i < NI; ++i) {
         const int e = (i * TPR + lane) * VEC;
         if (e < s.D) {
             count += (float)VEC;
-            if (w) wr[i] = load_raw<Tw, VEC>(w + wo + e);
-            if (b) br[i] = load_raw<Tw, VEC>(b + wo + e);
+            if (kHold && w) wr[i] = load_raw<Tw, VEC>(w + wo + e);
+            if (kHold && b) br[i] = load_raw<Tw, VEC>(b + wo + e);
         }
     }
-    auto fetch = [&](long long k) {
+    auto fetch = [&](long long k, Raw<T, VEC> (&next)[NI]) {
         if (!in || k >= per) return;
         const T* px = x + row_at(s, k, group) * s.D;
 #pragma unroll
@@ -323,10 +329,11 @@ ln_fwd_kernel(const T* __restrict__ x, const Tw* __restrict__ w, const Tw* __res
         }
     };
     const float inv_n = count > 0.f ? 1.f / count : 0.f, inv_d = 1.f / (float)s.D;
-    fetch(first);
+#pragma unroll
+    for (int d = 0; d < kDepth; ++d) fetch(first + d * step, next[d]);
     const Merge<TPR> merge(count, red[0][0]);
-    long long k = first;
-    for (long long turn = 0; turn < turns; ++turn, k += step) {
+    auto one = [&](long long turn, Raw<T, VEC> (&next)[NI]) {
+        const long long k = first + turn * step;
         const bool ok = in && k < per;
         Pair<VEC> xr[NI][P], sum = 0;
         float m, m2;
@@ -344,7 +351,7 @@ ln_fwd_kernel(const T* __restrict__ x, const Tw* __restrict__ w, const Tw* __res
 #pragma unroll
             for (int q = 0; q < P; ++q) sum = add2(sum, xr[i][q]);
         }
-        fetch(k + step);
+        fetch(k + kDepth * step, next);
         m = sum2(sum) * inv_n;
         const Pair<VEC> mm = splat<VEC>(-m);
         sum = 0;
@@ -372,10 +379,12 @@ ln_fwd_kernel(const T* __restrict__ x, const Tw* __restrict__ w, const Tw* __res
                     Pair<VEC> wp[P], bp[P];
                     float v[VEC];
                     if (w) {
+                        if (!kHold) wr[i] = load_raw<Tw, VEC>(w + wo + e);
                         unpack<VEC>(wr[i], v);
                         to_pairs<VEC>(v, wp);
                     }
                     if (b) {
+                        if (!kHold) br[i] = load_raw<Tw, VEC>(b + wo + e);
                         unpack<VEC>(br[i], v);
                         to_pairs<VEC>(v, bp);
                     }
@@ -396,6 +405,11 @@ ln_fwd_kernel(const T* __restrict__ x, const Tw* __restrict__ w, const Tw* __res
                 if (rstd) rstd[row] = r;
             }
         }
+    };
+    for (long long turn = 0; turn < turns; turn += kDepth) {
+#pragma unroll
+        for (int d = 0; d < kDepth; ++d)
+            if (turn + d < turns) one(turn + d, next[d]);
     }
 }
 
