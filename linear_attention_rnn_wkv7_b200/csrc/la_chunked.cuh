@@ -24,8 +24,9 @@
 // (below) each run on one warp per scheduler, at a third of its issue rate: latencies of
 // tensor memory, shared memory and barriers, and instruction fetch (see wait_slow).  At D = 128
 // it takes 4.1 us against 3 us.
-// B = 8, T = 4096, H = 64 of 64: 336 us, 3.3 TB/s, half of the measured copy rate (fp32
-// recurrence 3480 us); 16384 tokens of 16 heads of 128: 142 us with its states made beforehand.
+// B = 8, T = 4096, H = 64 of 64: 320 us, 3.4 TB/s, half of the measured copy rate (fp32
+// recurrence 3480 us); 16384 tokens of 16 heads of 128: 141 us with its states made beforehand.
+// The gradients' passes there: 300 us (dv), 430 us (dq, with states kept), 480 us (dk).
 // Tried and left: output staged in a tile of its own (the smaller ring cost as much); rows
 // of the decay scan on all lanes (slower: longer shuffles); waits as calls (each cost the MMA
 // warp 200 cycles more); score blocks of 32 columns (faster alone, slower with all SMs at it).
