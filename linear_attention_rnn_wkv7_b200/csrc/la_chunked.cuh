@@ -20,10 +20,10 @@
 // 2.5e-6.  Where it only makes bf16 results two parts do.
 //
 // What bounds it.  At D = 64 a chunk moves 64 KB from and to HBM (1.5 us at an SM's even share)
-// and takes about 1400 cycles of MMA; it takes 2.1 to 2.4 us, because the roles of a chunk
+// and takes about 1400 cycles of MMA; it takes 2.4 us, because the roles of a chunk
 // (below) each run on one warp per scheduler, at a third of its issue rate: latencies of
 // tensor memory, shared memory and barriers, and instruction fetch (see wait_slow).  At D = 128
-// it takes 4.1 us against 3 us.
+// it takes 4.6 us against 3 us.
 // B = 8, T = 4096, H = 64 of 64: 320 us, 3.4 TB/s, half of the measured copy rate (fp32
 // recurrence 3480 us); 16384 tokens of 16 heads of 128: 141 us with its states made beforehand.
 // The gradients' passes there: 300 us (dv), 430 us (dq, with states kept), 480 us (dk).

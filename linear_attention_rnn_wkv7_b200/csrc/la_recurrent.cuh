@@ -7,11 +7,15 @@
 // Unlike the delta rule, a token's update does not read the state, so tokens only meet in
 // an elementwise multiply-add: nothing but the issue rate of the 3 D^2 fp32 operations per
 // token bounds a block, and shared memory must feed them.  A block owns 64 columns of one
-// (segment, head); a thread holds a tile of 16 rows x 4 columns (64 registers), so the 16
+// (segment, head); a thread holds a tile of 16 rows x 4 columns (64 registers), so the 8
 // float4 of x and y that it reads per token serve 192 operations (one column per thread
 // would read as many for 48).  The D / 16 row parts of a column are adjacent lanes; their
 // sums meet by shuffles.  Parts of a staged row are 20 floats apart, so the parts that
 // read together sit in different banks.
+//
+// fp32, B = 2, T = 333, H = 8 of 64: 115 us in one chain per head (0.34 us a token), 32 us in
+// 32-token segments.  bf16 B = 8, T = 4096, H = 64 here: 3.48 ms, 0.72 ms of it the issue
+// rate's floor.
 //
 // Tokens are staged in tiles (fp32, the decay's exponential taken once); the next tile's
 // global loads are in registers while the current one runs.  Outputs leave through
