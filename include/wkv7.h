@@ -395,9 +395,11 @@ wkv7_status wkv7_gdn_bwd(const void* q, const void* k, const void* v, const void
  *   o              [B, T, H, V]  dtype   output (must not alias an input)
  *   sT             [N, H, K, V]  fp32    final states, or NULL to skip; may equal s0
  *   cu_seqlens, N, layout, algo          as for wkv7_fwd; a sequence may be empty.  If an
- *                                        entry is out of order or range the whole call is
- *                                        skipped (WKV7_ERR_DEVICE_BAD_SEQLENS); rows behind
- *                                        the last sequence are left as they are.
+ *                                        entry is out of order or range or cu_seqlens[0] is
+ *                                        not 0, the whole call is skipped
+ *                                        (WKV7_ERR_DEVICE_BAD_SEQLENS); cu_seqlens[N] may be
+ *                                        less than T: rows behind the last sequence are left
+ *                                        as they are.
  *   scale                                any finite number
  *   workspace      at least wkv7_la_fwd_workspace_bytes(..) bytes, 16-byte aligned (NULL
  *                  when that is 0): start states of the segments that long sequences are
@@ -548,6 +550,20 @@ wkv7_status wkv7_test_stall_next_chunked(int tid);
  */
 wkv7_status wkv7_test_chunked_schedule(long long units, int len, int* resident, long long* ctas,
                                        long long* cmax);
+
+/*
+ * wkv7_test_la_pieces -- test hook (no counterpart on the pages): the work of block `block`
+ * of a pass of the decay linear attention (wkv7_la_fwd; backward = 1: a pass against time),
+ * computed on the host by the kernels' own code for a GPU of 148 SMs.  cu_seqlens is HOST
+ * memory here, or NULL.  A piece is six numbers: sequence, head, first token and the token
+ * behind the last one within the sequence, and whether it holds the sequence's first and its
+ * last chunk in the pass's direction.  At most max_pieces are written to `pieces`; *count
+ * receives how many, *blocks how many blocks there are, *skipped whether the kernels skip the
+ * call because of its offsets.  All pointers are host memory.  Launches nothing.
+ */
+wkv7_status wkv7_test_la_pieces(int B, int T, int H, int K, const int32_t* cu_seqlens, int N,
+                                wkv7_dtype dtype, int backward, int block, int32_t* pieces,
+                                int max_pieces, int* count, int* blocks, int* skipped);
 
 #ifdef __cplusplus
 }

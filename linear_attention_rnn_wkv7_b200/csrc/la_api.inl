@@ -170,6 +170,35 @@ wkv7_status wkv7_la_step(const void* q, const void* k, const void* v, const void
                                                            stream));
 }
 
+wkv7_status wkv7_test_la_pieces(int B, int T, int H, int K, const int32_t* cu_seqlens, int N,
+                                wkv7_dtype dtype, int backward, int block, int32_t* pieces,
+                                int max_pieces, int* count, int* blocks, int* skipped) {
+    using namespace wkv7::la;
+    if (!pieces || !count || !blocks || !skipped || max_pieces < 0 || block < 0)
+        return WKV7_ERR_INVALID_ARG;
+    Problem p;
+    const wkv7_status st = la_problem(p, B, T, H, K, K, cu_seqlens != nullptr, cu_seqlens, N, 0,
+                                      dtype, WKV7_ALGO_AUTO);
+    if (st != WKV7_OK) return st;
+    const Geom& g = p.geom;
+    const Plan plan = make_plan(p);
+    *count = *skipped = 0;
+    for (int i = 0; cu_seqlens && i < N; ++i) *skipped |= seqlen_bad(g, i);
+    // the recurrent kernel has a block for each segment and head (and column slab)
+    *blocks = (int)(p.chunked ? tc::blocks_of(g, plan.seg, plan.run, kBlocks)
+                              : g.slots(plan.seg) * g.H);
+    if (block >= *blocks) return WKV7_OK;
+    tc::Cursor at = tc::first_cursor(g, plan.seg, plan.run, block, *blocks);
+    while (*count < max_pieces) {
+        const tc::Piece s = tc::next_piece(g, plan.seg, at, backward != 0, 0);
+        if (s.chunks < 0) break;
+        const int32_t row[6] = {s.it.n, s.h, s.tb, s.te, s.begins, s.ends};
+        for (int i = 0; i < 6; ++i) pieces[6 * *count + i] = row[i];
+        ++*count;
+    }
+    return WKV7_OK;
+}
+
 // ---- layer norm -------------------------------------------------------------------------
 static wkv7_status ln_check(long long rows, long long groups, long long inner, long long D,
                             wkv7_dtype dtype, wkv7_dtype wdtype) {

@@ -310,16 +310,39 @@ struct Piece {
 struct Cursor {
     int item, items;  // segments; or positions: the next one, the run's first
     int slots;        // of the chunks (runs), 0: segments
+    int step;         // segments: blocks
 };
+// Blocks of a pass on a device of `sms` SMs.
+inline long long blocks_of(const Geom& g, int seg, int run, int sms) {
+    const long long items = g.slots(run > 0 ? kChunk : seg) * g.H;
+    return run > 0 ? (items + run - 1) / run : items < sms ? items : sms;
+}
+// Where block `block` of `blocks` begins.
+__host__ __device__ __forceinline__ Cursor first_cursor(const Geom& g, int seg, int run, int block,
+                                                        int blocks) {
+    Cursor at;
+    at.step = blocks;
+    if (run == 0) {
+        at.slots = 0;
+        at.item = block - blocks;
+        at.items = (int)(g.slots(seg) * g.H);
+    } else {
+        at.slots = (int)g.slots(kChunk);
+        const long long all = (long long)at.slots * g.H, start = (long long)block * run;
+        at.items = (int)start;
+        at.item = (int)(start + run < all ? start + run : all) - 1;
+    }
+    return at;
+}
 // The cursor's next piece; chunks < 0: none left.  Out of line: divisions, in every role.
-__device__ __noinline__ Piece next_piece(const Geom& g, int seg, Cursor& at, int rev, int state_only) {
+__host__ __device__ __noinline__ Piece next_piece(const Geom& g, int seg, Cursor& at, int rev, int state_only) {
     Piece s;
     s.tb = s.te = 0;
     s.chunks = -1;
     s.begins = s.ends = false;
     if (at.slots == 0) {
-        while (at.items - at.item > (int)gridDim.x) {
-            at.item += gridDim.x;
+        while (at.items - at.item > at.step) {
+            at.item += at.step;
             s.slot = at.item / g.H;
             s.h = at.item - s.slot * g.H;
             s.it = locate(g, s.slot, seg);
@@ -362,19 +385,8 @@ template <bool kRev, bool kStateOnly>
 struct Walk : Piece {
     Cursor at;
     template <typename P>
-    __device__ __forceinline__ explicit Walk(const P& p) {
-        const Geom& g = p.geom;
-        if (kStateOnly || p.run == 0) {
-            at.slots = 0;
-            at.item = (int)blockIdx.x - (int)gridDim.x;
-            at.items = (int)(g.slots(p.seg) * g.H);
-        } else {
-            at.slots = (int)g.slots(kChunk);
-            const long long all = (long long)at.slots * g.H, start = (long long)blockIdx.x * p.run;
-            at.items = (int)start;
-            at.item = (int)(start + p.run < all ? start + p.run : all) - 1;
-        }
-    }
+    __device__ __forceinline__ explicit Walk(const P& p)
+        : at(first_cursor(p.geom, p.seg, kStateOnly ? 0 : p.run, (int)blockIdx.x, (int)gridDim.x)) {}
     // The next piece; false: none left.
     template <typename P>
     __device__ __forceinline__ bool next(const P& p) {
@@ -1340,11 +1352,7 @@ inline cudaError_t launch_d(const Pass<__nv_bfloat16>& p, int B, cudaStream_t st
     const void* ptr[4] = {kStateOnly ? p.y : p.x, p.y, p.z, kStateOnly ? p.y : p.out};
     for (int i = 0; i < 4; ++i)
         if (!make_map(&m[i], ptr[i], B, p.geom, D)) return cudaErrorInvalidValue;
-    const bool runs = !kStateOnly && p.run > 0;
-    const long long items = p.geom.slots(runs ? kChunk : p.seg) * p.geom.H;
-    const unsigned grid = (unsigned)(runs          ? (items + p.run - 1) / p.run
-                                     : items < sms ? items
-                                                   : sms);
+    const unsigned grid = (unsigned)blocks_of(p.geom, p.seg, kStateOnly ? 0 : p.run, sms);
     la_chunked_kernel<D, kRev, kStateOnly, kGrad><<<grid, kThreads, Cfg<D>::kBytes, stream>>>(m[0], m[1], m[2],
                                                                                  m[3], p);
     return cudaGetLastError();

@@ -67,19 +67,21 @@ struct Item {
     int bb;         // batch row of the inputs
 };
 
-// Whether cu_seqlens is non-decreasing within [0, T]; every thread of the block calls it.
+// Whether sequence i's offsets are out of order or range, or the first is not 0.
+__host__ __device__ __forceinline__ bool seqlen_bad(const Geom& g, int i) {
+    const int a = g.cu[i], b = g.cu[i + 1];
+    return (a < 0) | (b < a) | (b > g.T) | ((i == 0) & (a != 0));
+}
+// Whether cu_seqlens is non-decreasing from 0 within [0, T]; every thread of the block calls it.
 __device__ __forceinline__ bool seqlens_ok(const Geom& g, int tid, int threads) {
     if (!g.cu) return true;
     int bad = 0;
-    for (int i = tid; i < g.N; i += threads) {
-        const int a = g.cu[i], b = g.cu[i + 1];
-        bad |= (a < 0) | (b < a) | (b > g.T);
-    }
+    for (int i = tid; i < g.N; i += threads) bad |= seqlen_bad(g, i);
     return !__syncthreads_or(bad);
 }
 
 // (Slot numbers fit 32 bits: the entry points check.)
-__device__ __forceinline__ Item locate(const Geom& g, int slot, int seg) {
+__host__ __device__ __forceinline__ Item locate(const Geom& g, int slot, int seg) {
     Item it;
     if (!g.cu) {
         it.nseg = Geom::segs(g.T, seg);
@@ -101,7 +103,8 @@ __device__ __forceinline__ Item locate(const Geom& g, int slot, int seg) {
     it.j = slot - it.bos / seg - lo;
     it.nseg = Geom::segs(it.len, seg);
     it.bb = 0;
-    if (it.j >= it.nseg) it.n = -1;
+    // between two sequences' slots, or (offsets that do not begin at 0) before the first's
+    if (it.j < 0 || it.j >= it.nseg) it.n = -1;
     return it;
 }
 __device__ __forceinline__ long long slot_of(const Geom& g, const Item& it, int j, int seg) {

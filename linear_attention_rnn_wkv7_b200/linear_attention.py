@@ -73,7 +73,7 @@ def wkv7_la_fwd(q, k, v, g, s0=None, mask=None, cu_seqlens=None, output_final_st
     """Linear attention with a decay for each head.  q, k [B,T,H,K]; v [B,T,H,V]; g [B,T,H] (log
     decay of each token) or [H] (of each head), bf16 or fp32, all alike; [B,H,T,*] and
     [B,H,T] with head_first; s0 [N,H,K,V] fp32 or None; mask [B,T] uint8/bool or None (0: the
-    state stays); cu_seqlens [N+1] int32 (B must be 1) or None.  K = V in {64, 128, 256}.
+    state stays); cu_seqlens [N+1] int32 from 0 (B must be 1) or None.  K = V in {64, 128, 256}.
     The workspace (uint8, wkv7_la_workspace_bytes) is allocated here when not given.
     Returns (o shaped like v, sT [N,H,K,V] fp32 or None)."""
     B, T, H, K, V, N, per_head, mask = _sizes(q, k, v, g, s0, mask, cu_seqlens, head_first)

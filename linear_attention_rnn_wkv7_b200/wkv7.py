@@ -98,6 +98,8 @@ def library() -> ctypes.CDLL:
                                                                         p])
         lib.wkv7_la_step.restype = i
         lib.wkv7_la_step.argtypes = [p] * 4 + [i] + [p] * 3 + [i, i, i, i, f, i, p]
+        lib.wkv7_test_la_pieces.restype = i
+        lib.wkv7_test_la_pieces.argtypes = [i, i, i, i, p, i, i, i, i, p, i, p, p, p]
         lib.wkv7_ln_fwd.restype = i
         lib.wkv7_ln_fwd.argtypes = [p] * 6 + [ll, i, ll, i, f, i, i, p]
         lib.wkv7_ln_bwd_workspace_bytes.restype = sz
