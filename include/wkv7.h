@@ -554,12 +554,14 @@ wkv7_status wkv7_test_chunked_schedule(long long units, int len, int* resident, 
 /*
  * wkv7_test_la_pieces -- test hook (no counterpart on the pages): the work of block `block`
  * of a pass of the decay linear attention (wkv7_la_fwd; backward = 1: a pass against time),
- * computed on the host by the kernels' own code for a GPU of 148 SMs.  cu_seqlens is HOST
- * memory here, or NULL.  A piece is six numbers: sequence, head, first token and the token
- * behind the last one within the sequence, and whether it holds the sequence's first and its
- * last chunk in the pass's direction.  At most max_pieces are written to `pieces`; *count
- * receives how many, *blocks how many blocks there are, *skipped whether the kernels skip the
- * call because of its offsets.  All pointers are host memory.  Launches nothing.
+ * computed on the host by the kernels' own code for a GPU of 148 SMs.  Where sequences are
+ * cut into equal runs, a block is one; else the blocks share a list, and block 0 stands for all
+ * of them.  cu_seqlens is HOST memory here, or NULL.  A piece is six numbers: sequence, head,
+ * first token and the token behind the last one within the sequence, and whether it holds the
+ * sequence's first and its last chunk in the pass's direction.  At most max_pieces are
+ * written to `pieces`; *count receives how many, *blocks how many blocks there are, *skipped
+ * whether the kernels skip the call because of its offsets.  All pointers are host memory.
+ * Launches nothing.
  */
 wkv7_status wkv7_test_la_pieces(int B, int T, int H, int K, const int32_t* cu_seqlens, int N,
                                 wkv7_dtype dtype, int backward, int block, int32_t* pieces,

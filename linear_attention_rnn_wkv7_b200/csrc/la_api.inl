@@ -184,11 +184,10 @@ wkv7_status wkv7_test_la_pieces(int B, int T, int H, int K, const int32_t* cu_se
     const Plan plan = make_plan(p);
     *count = *skipped = 0;
     for (int i = 0; cu_seqlens && i < N; ++i) *skipped |= seqlen_bad(g, i);
-    // the recurrent kernel has a block for each segment and head (and column slab)
-    *blocks = (int)(p.chunked ? tc::blocks_of(g, plan.seg, plan.run, kBlocks)
-                              : g.slots(plan.seg) * g.H);
+    // runs: a block each; segments (and all of the recurrent kernel's work): the whole list
+    *blocks = plan.run > 0 ? (int)plan.blocks : 1;
     if (block >= *blocks) return WKV7_OK;
-    tc::Cursor at = tc::first_cursor(g, plan.seg, plan.run, block, *blocks);
+    tc::Cursor at = tc::first_cursor(g, plan.seg, plan.run, block);
     while (*count < max_pieces) {
         const tc::Piece s = tc::next_piece(g, plan.seg, at, backward != 0, 0);
         if (s.chunks < 0) break;

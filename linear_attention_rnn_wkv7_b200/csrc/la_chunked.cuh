@@ -310,21 +310,22 @@ struct Piece {
 struct Cursor {
     int item, items;  // segments; or positions: the next one, the run's first
     int slots;        // of the chunks (runs), 0: segments
-    int step;         // segments: blocks
 };
-// Blocks of a pass on a device of `sms` SMs.
-inline long long blocks_of(const Geom& g, int seg, int run, int sms) {
-    const long long items = g.slots(run > 0 ? kChunk : seg) * g.H;
-    return run > 0 ? (items + run - 1) / run : items < sms ? items : sms;
+// Blocks that share the segments; on the host, where a test walks them, one has them all.  (As a
+// number in the cursor it cost the gradients' kernels 40 to 80 bytes of spills.)
+__host__ __device__ __forceinline__ int grid_blocks() {
+#ifdef __CUDA_ARCH__
+    return (int)gridDim.x;
+#else
+    return 1;
+#endif
 }
-// Where block `block` of `blocks` begins.
-__host__ __device__ __forceinline__ Cursor first_cursor(const Geom& g, int seg, int run, int block,
-                                                        int blocks) {
+// Where a block begins.
+__host__ __device__ __forceinline__ Cursor first_cursor(const Geom& g, int seg, int run, int block) {
     Cursor at;
-    at.step = blocks;
     if (run == 0) {
         at.slots = 0;
-        at.item = block - blocks;
+        at.item = block - grid_blocks();
         at.items = (int)(g.slots(seg) * g.H);
     } else {
         at.slots = (int)g.slots(kChunk);
@@ -341,8 +342,8 @@ __host__ __device__ __noinline__ Piece next_piece(const Geom& g, int seg, Cursor
     s.chunks = -1;
     s.begins = s.ends = false;
     if (at.slots == 0) {
-        while (at.items - at.item > at.step) {
-            at.item += at.step;
+        while (at.items - at.item > grid_blocks()) {
+            at.item += grid_blocks();
             s.slot = at.item / g.H;
             s.h = at.item - s.slot * g.H;
             s.it = locate(g, s.slot, seg);
@@ -386,7 +387,7 @@ struct Walk : Piece {
     Cursor at;
     template <typename P>
     __device__ __forceinline__ explicit Walk(const P& p)
-        : at(first_cursor(p.geom, p.seg, kStateOnly ? 0 : p.run, (int)blockIdx.x, (int)gridDim.x)) {}
+        : at(first_cursor(p.geom, p.seg, kStateOnly ? 0 : p.run, (int)blockIdx.x)) {}
     // The next piece; false: none left.
     template <typename P>
     __device__ __forceinline__ bool next(const P& p) {
@@ -1352,7 +1353,11 @@ inline cudaError_t launch_d(const Pass<__nv_bfloat16>& p, int B, cudaStream_t st
     const void* ptr[4] = {kStateOnly ? p.y : p.x, p.y, p.z, kStateOnly ? p.y : p.out};
     for (int i = 0; i < 4; ++i)
         if (!make_map(&m[i], ptr[i], B, p.geom, D)) return cudaErrorInvalidValue;
-    const unsigned grid = (unsigned)blocks_of(p.geom, p.seg, kStateOnly ? 0 : p.run, sms);
+    const bool runs = !kStateOnly && p.run > 0;
+    const long long items = p.geom.slots(runs ? kChunk : p.seg) * p.geom.H;
+    const unsigned grid = (unsigned)(runs          ? (items + p.run - 1) / p.run
+                                     : items < sms ? items
+                                                   : sms);
     la_chunked_kernel<D, kRev, kStateOnly, kGrad><<<grid, kThreads, Cfg<D>::kBytes, stream>>>(m[0], m[1], m[2],
                                                                                  m[3], p);
     return cudaGetLastError();
