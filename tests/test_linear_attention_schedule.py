@@ -21,8 +21,8 @@ def clib():
 def walk(clib, T, H, N, cu=None, D=64, dtype=BF16, backward=False):
     """Every block's pieces, and whether the kernels skip the call."""
     host = None if cu is None else (ctypes.c_int32 * len(cu))(*cu)
-    # no block has more pieces than the problem has (slot, head) pairs
-    most = (T // 32 + 2 * N + 1) * H + 1
+    # no walk has more pieces than the problem has (segment, head) pairs; segments have 32 tokens or more
+    most = (T // 32 + 2) * N * H + 1
     room = (ctypes.c_int32 * (6 * most))()
     count, blocks, skipped = ctypes.c_int(), ctypes.c_int(1), ctypes.c_int()
     pieces, block = [], 0
