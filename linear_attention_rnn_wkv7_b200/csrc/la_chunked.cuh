@@ -820,10 +820,15 @@ la_chunked_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constan
                     sc->out[blk] = ow;
                     sc->kb[blk] = p.key_scale * ex2(kLog2e * (kRev ? before + tail : after));
                 }
-                // (1 + the small difference: a constant decay's rounding repeats every chunk)
+                // A weak decay's rounding repeats at every chunk that a state lives through: 1 +
+                // the small difference, off by half a step of a number near 1 (2^-25; expf's
+                // steps are up to four times that).  A strong one is e^sum itself: the
+                // difference would be -1 rounded, off by 2^-25 of 1 and not of e^sum (7e-3
+                // of it at a sum of -12.8).
                 if (lane == 0) {
                     sc->more = i + 1 < chunks || have;
-                    sc->decay = 1.f + expm1f((t0s + t1s) + (t2s + t3s));
+                    const float sum = (t0s + t1s) + (t2s + t3s);
+                    sc->decay = fabsf(sum) < 0.5f ? 1.f + expm1f(sum) : expf(sum);
                 }
                 // rows of Z that do not enter may hold anything (0 * NaN is NaN): clear them
                 if (__any_sync(0xffffffffu, enter != 15u)) {
