@@ -245,7 +245,9 @@ struct Merge {
         const float d = __shfl_xor_sync(0xffffffffu, mean, m) - mean;
         m2 += __shfl_xor_sync(0xffffffffu, m2, m);
         mean = fmaf(d, r[l], mean);
-        m2 = fmaf(d * d, c[l], m2);
+        // (c d first: 0 for a thread without elements, where d, the mean itself, may have a
+        // square beyond fp32)
+        m2 = fmaf(c[l] * d, d, m2);
     }
     // Mean and sum of squares around it over the team, from each thread's; all get the same.
     __device__ __forceinline__ void operator()(float& mean, float& m2, float (*red)[32]) const {
