@@ -422,6 +422,20 @@ wkv7_status wkv7_la_fwd(const void* q, const void* k, const void* v, const void*
                         size_t workspace_bytes, void* stream);
 
 /*
+ * wkv7_la_zero_tail -- zeros in the rows behind the last packed sequence, which wkv7_la_fwd and
+ * wkv7_la_bwd leave as they are: for outputs and gradients in memory that holds nothing yet.
+ *
+ *   x0, x1, x2     [1, T, H, K]  dtype   or NULL
+ *   scalars        [1, T, H]     dtype   or NULL; needs only element alignment
+ *   cu_seqlens, N, layout                as for wkv7_la_fwd; nothing is written when an entry is
+ *                                        out of order or range (the calls above report it).
+ *                                        N = 0: all rows
+ */
+wkv7_status wkv7_la_zero_tail(void* x0, void* x1, void* x2, void* scalars, int T, int H, int K,
+                              const int32_t* cu_seqlens, int N, wkv7_layout layout,
+                              wkv7_dtype dtype, void* stream);
+
+/*
  * wkv7_la_step -- one decode token of the same recurrence for B independent states.
  *
  *   q, k           [B, H, K]     dtype

@@ -147,6 +147,32 @@ wkv7_status wkv7_la_bwd(const void* q, const void* k, const void* v, const void*
     return status_of(p.bf16 ? run(__nv_bfloat16()) : run(float()));
 }
 
+wkv7_status wkv7_la_zero_tail(void* x0, void* x1, void* x2, void* scalars, int T, int H, int K,
+                              const int32_t* cu_seqlens, int N, wkv7_layout layout,
+                              wkv7_dtype dtype, void* stream_) {
+    wkv7::la::Problem p;
+    if (!layout_ok(layout)) return WKV7_ERR_INVALID_ARG;
+    const wkv7_status st = la_problem(p, 1, T, H, K, K, 1, cu_seqlens, N,
+                                      layout == WKV7_LAYOUT_BHTK, dtype, WKV7_ALGO_AUTO);
+    if (st != WKV7_OK) return st;
+    if (p.rows() == 0) return WKV7_OK;
+    if (!cu_seqlens || (reinterpret_cast<uintptr_t>(cu_seqlens) & 3u) != 0 || !aligned16(x0) ||
+        !aligned16(x1) || !aligned16(x2) || (scalars && !ok_scalar_ptr(scalars, dtype)))
+        return WKV7_ERR_INVALID_ARG;
+    cudaStream_t stream = static_cast<cudaStream_t>(stream_);
+    auto run = [&](auto zero) {
+        using T_ = decltype(zero);
+        const wkv7::la::Tail<T_> t{{static_cast<T_*>(x0), static_cast<T_*>(x1), static_cast<T_*>(x2)},
+                                   static_cast<T_*>(scalars), K};
+        // 4 KB a block and turn; the tail's length is on the device
+        const long long want = p.rows() * K / 2048 + 1;
+        const unsigned blocks = (unsigned)(want < 296 ? want : 296);
+        wkv7::la::la_tail_kernel<T_><<<blocks, 256, 0, stream>>>(p.geom, t);
+        return cudaGetLastError();
+    };
+    return status_of(p.bf16 ? run(__nv_bfloat16()) : run(float()));
+}
+
 wkv7_status wkv7_la_step(const void* q, const void* k, const void* v, const void* g, int g_per_head,
                          const float* state, float* out_state, void* o, int B, int H, int K, int V,
                          float scale, wkv7_dtype dtype, void* stream_) {

@@ -304,5 +304,37 @@ la_dg_sum_kernel(Geom g, const float* __restrict__ part, long long slots, Tin* _
     }
 }
 
+// ---- rows behind the last sequence ---------------------------------------------------------
+// Zeros in the rows behind the last packed sequence of up to three [.., D] tensors and one of a
+// value per token and head; nullptr: none.  They are one stretch of memory (token-major) or one
+// a head; D-wide rows are whole 16-byte groups.
+template <typename Tin>
+struct Tail {
+    Tin* x[3];
+    Tin* s;
+    int D;
+};
+template <typename Tin>
+__global__ void __launch_bounds__(256) la_tail_kernel(Geom g, Tail<Tin> t) {
+    if (!seqlens_ok(g, threadIdx.x, 256)) return;
+    constexpr int kVec = 16 / sizeof(Tin);
+    const long long end = g.N > 0 ? g.cu[g.N] : 0;
+    const int parts = g.head_first ? g.H : 1;
+    const long long width = g.head_first ? 1 : g.H;          // values of a token in a part
+    const long long n = (g.T - end) * width, at = end * width, stride = g.T * width;
+    const long long first = (long long)blockIdx.x * 256 + threadIdx.x, step = (long long)gridDim.x * 256;
+    for (int i = 0; i < 3; ++i) {
+        if (!t.x[i]) continue;
+        const long long v = n * (t.D / kVec);
+        for (int h = 0; h < parts; ++h) {
+            uint4* to = reinterpret_cast<uint4*>(t.x[i] + (h * stride + at) * t.D);
+            for (long long e = first; e < v; e += step) to[e] = make_uint4(0, 0, 0, 0);
+        }
+    }
+    if (t.s)
+        for (int h = 0; h < parts; ++h)
+            for (long long e = first; e < n; e += step) t.s[h * stride + at + e] = from_f32<Tin>(0.f);
+}
+
 }  // namespace la
 }  // namespace wkv7

@@ -58,6 +58,16 @@ def _workspace(given, nbytes, ref):
     return given
 
 
+def _zero_tail(x, scalars, T, H, K, cu_seqlens, N, head_first):
+    """Zeros in the rows behind the last sequence of up to three fresh tensors and one of scalars."""
+    x = list(x) + [None] * (3 - len(x))
+    st = library().wkv7_la_zero_tail(*(address(t) for t in x), address(scalars), T, H, K,
+                                     address(cu_seqlens), N, int(bool(head_first)),
+                                     _dtype_code(x[0]), stream(x[0]))
+    if st != OK:
+        raise WKV7Error(st, "wkv7_la_zero_tail")
+
+
 def wkv7_la_workspace_bytes(B, T, H, K=64, V=64, N=None, packed=False, dtype=torch.bfloat16,
                             algo: str = "auto", backward: bool = False) -> int:
     """Workspace bytes of wkv7_la_fwd or, with backward, of wkv7_la_bwd."""
@@ -74,10 +84,12 @@ def wkv7_la_fwd(q, k, v, g, s0=None, mask=None, cu_seqlens=None, output_final_st
     decay of each token) or [H] (of each head), bf16 or fp32, all alike; [B,H,T,*] and
     [B,H,T] with head_first; s0 [N,H,K,V] fp32 or None; mask [B,T] uint8/bool or None (0: the
     state stays); cu_seqlens [N+1] int32 from 0 (B must be 1) or None.  K = V in {64, 128, 256}.
-    The workspace (uint8, wkv7_la_workspace_bytes) is allocated here when not given.
+    The workspace (uint8, wkv7_la_workspace_bytes) is allocated here when not given.  Rows behind
+    the last packed sequence are 0 in an o that is allocated here and left alone in one given.
     Returns (o shaped like v, sT [N,H,K,V] fp32 or None)."""
     B, T, H, K, V, N, per_head, mask = _sizes(q, k, v, g, s0, mask, cu_seqlens, head_first)
-    if o is None:
+    fresh = o is None
+    if fresh:
         o = torch.empty_like(v)
     else:
         expect(o, "o", q.dtype, v.shape, q)
@@ -94,6 +106,8 @@ def wkv7_la_fwd(q, k, v, g, s0=None, mask=None, cu_seqlens=None, output_final_st
                              address(mask), address(o), address(sT), B, T, H, K, V, address(cu_seqlens), N,
                              float(scale), int(bool(head_first)), _dtype_code(q), ALGO[algo],
                              address(ws), 0 if ws is None else ws.numel(), stream(q))
+        if st == OK and fresh and cu_seqlens is not None:
+            _zero_tail([o], None, T, H, K, cu_seqlens, N, head_first)
     if st != OK:
         raise WKV7Error(st, "wkv7_la_fwd")
     return o, sT
@@ -134,7 +148,8 @@ def wkv7_la_bwd(q, k, v, g, dout, s0=None, mask=None, dsT=None, cu_seqlens=None,
                 need_dg: bool = True, need_ds0: bool = True):
     """Backward of wkv7_la_fwd for L = sum(o * dout) + sum(S_T * dsT).  Returns a dict: dq, dk, dv,
     dg (input dtype, shaped like the inputs; dg of a [H] g is summed over batch and tokens) and
-    ds0 (fp32 [N,H,K,V]); dg and ds0 are None when not needed."""
+    ds0 (fp32 [N,H,K,V]); dg and ds0 are None when not needed.  Rows behind the last packed
+    sequence have gradients of 0."""
     B, T, H, K, V, N, per_head, mask = _sizes(q, k, v, g, s0, mask, cu_seqlens, head_first)
     expect(dout, "dout", q.dtype, v.shape, q)
     if dsT is not None:
@@ -154,6 +169,9 @@ def wkv7_la_bwd(q, k, v, g, dout, s0=None, mask=None, dsT=None, cu_seqlens=None,
                              address(cu_seqlens), N, float(scale), int(bool(head_first)),
                              _dtype_code(q), ALGO[algo], address(ws),
                              0 if ws is None else ws.numel(), stream(q))
+        if st == OK and cu_seqlens is not None:
+            _zero_tail([out["dq"], out["dk"], out["dv"]], None if per_head else out["dg"], T, H, K,
+                       cu_seqlens, N, head_first)
     if st != OK:
         raise WKV7Error(st, "wkv7_la_bwd")
     return out

@@ -96,6 +96,8 @@ def library() -> ctypes.CDLL:
         lib.wkv7_la_bwd.restype = i
         lib.wkv7_la_bwd.argtypes = ([p] * 4 + [i] + [p] * 9 + [i] * 5 + [p, i, f, i, i, i, p, sz,
                                                                         p])
+        lib.wkv7_la_zero_tail.restype = i
+        lib.wkv7_la_zero_tail.argtypes = [p] * 4 + [i, i, i, p, i, i, i, p]
         lib.wkv7_la_step.restype = i
         lib.wkv7_la_step.argtypes = [p] * 4 + [i] + [p] * 3 + [i, i, i, i, f, i, p]
         lib.wkv7_test_la_pieces.restype = i

@@ -46,3 +46,48 @@ def test_state_carried_through_a_strong_chunk(cuda_device, algo, D, B, T, H, str
         assert not bool(bad.any()), (name, float(((got.double() - want) / want).abs().max()),
                                      float(tol.max()))
     assert lib.wkv7_get_last_error() == OK
+
+
+# --------------------------------------------------------------- rows behind the last sequence
+def dirty(*like):
+    """Leaves NaN in memory that the next allocations of these shapes are likely to get."""
+    for t in like:
+        for _ in range(4):
+            torch.full_like(t, float("nan"))
+    torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("dtype,D", [(F32, 64), (BF16, 64), (BF16, 128)])
+@pytest.mark.parametrize("head_first", [False, True])
+@pytest.mark.parametrize("cu", [[0, 70, 200], [0, 0, 0], [0], [0, 200, 333]])
+def test_rows_behind_the_last_sequence_are_zero(cuda_device, dtype, D, head_first, cu):
+    """What the binding allocates is defined everywhere: no output and no gradient behind the last
+    sequence, so that the norm behind it and the layers before it stay finite."""
+    gen = torch.Generator().manual_seed(4)
+    T, H, end = 333, 3, cu[-1]
+    lead = (1, H, T) if head_first else (1, T, H)
+    x = {n: torch.randn(*lead, D, generator=gen).to(dtype).cuda() for n in ("q", "k", "v", "do")}
+    x["g"] = -torch.rand(*lead, generator=gen).to(dtype).cuda()
+    cu_t = torch.tensor(cu, dtype=torch.int32, device="cuda")
+    rows = (lambda t: t.transpose(1, 2)) if head_first else (lambda t: t)
+    dirty(*x.values())
+    o, _ = lib.wkv7_la_fwd(x["q"], x["k"], x["v"], x["g"], cu_seqlens=cu_t, head_first=head_first)
+    assert bool((rows(o)[:, end:] == 0).all())
+    dirty(*x.values())
+    r = lib.wkv7_la_bwd(x["q"], x["k"], x["v"], x["g"], x["do"], cu_seqlens=cu_t,
+                        head_first=head_first)
+    for n in ("dq", "dk", "dv", "dg"):
+        assert bool((rows(r[n])[:, end:] == 0).all()), n
+
+    w, b = (torch.randn(H, D, generator=gen).cuda() for _ in range(2))
+    a = {n: t.clone().requires_grad_() for n, t in {**x, "w": w, "b": b}.items() if n != "do"}
+    dirty(*x.values())
+    y, _ = lib.decay_linear_attention(a["q"], a["k"], a["v"], a["g"], cu_seqlens=cu_t,
+                                      head_first=head_first, norm=(a["w"], a["b"], 1e-5))
+    dirty(*x.values())
+    rows(y)[:, :end].backward(rows(x["do"])[:, :end])
+    for n, t in a.items():
+        assert bool(torch.isfinite(t.grad).all()), n
+    for n in ("q", "k", "v", "g"):
+        assert bool((rows(a[n].grad)[:, end:] == 0).all()), n
+    assert lib.wkv7_get_last_error() == OK

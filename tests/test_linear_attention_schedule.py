@@ -7,7 +7,8 @@ import torch
 
 import linear_attention_rnn_wkv7_b200 as lib
 from linear_attention_rnn_wkv7_b200 import build as lib_build
-from linear_attention_rnn_wkv7_b200.wkv7 import ERR_DEVICE_BAD_SEQLENS, OK
+from linear_attention_rnn_wkv7_b200.wkv7 import (ERR_DEVICE_BAD_SEQLENS, ERR_INVALID_ARG,
+                                                 ERR_UNSUPPORTED, OK)
 
 F32, BF16 = 1, 0
 
@@ -109,6 +110,24 @@ def test_order_and_range(clib, cu, bad):
     assert clib.wkv7_test_la_pieces(1, 900, 2, 64, host, 3, BF16, 0, 0, one, 0, ctypes.byref(n),
                                     ctypes.byref(n), ctypes.byref(skipped)) == OK
     assert bool(skipped.value) == bad
+
+
+P = 0x7f0000000000
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(x0=P + 8), ERR_INVALID_ARG), (dict(x2=P + 2), ERR_INVALID_ARG), (dict(s=P + 1), ERR_INVALID_ARG),
+    (dict(cu=0), ERR_INVALID_ARG), (dict(cu=P + 2), ERR_INVALID_ARG), (dict(T=-1), ERR_INVALID_ARG),
+    (dict(H=0), ERR_INVALID_ARG), (dict(N=-1), ERR_INVALID_ARG), (dict(layout=2), ERR_INVALID_ARG),
+    (dict(dtype=2), ERR_INVALID_ARG), (dict(K=96), ERR_UNSUPPORTED), (dict(T=0), OK),
+])
+def test_zero_tail_refuses(clib, kw, status):
+    a = dict(x0=P, x1=P + (1 << 20), x2=P + (2 << 20), s=P + 4096, T=64, H=4, K=64, cu=P + 64, N=2,
+             layout=0, dtype=0)
+    a.update(kw)
+    assert clib.wkv7_la_zero_tail(*(ctypes.c_void_p(a[n]) for n in ("x0", "x1", "x2", "s")), a["T"],
+                                  a["H"], a["K"], ctypes.c_void_p(a["cu"]), a["N"], a["layout"],
+                                  a["dtype"], None) == status
 
 
 @pytest.mark.gpu
