@@ -9,7 +9,7 @@ import torch
 from torch.autograd.function import once_differentiable
 
 from ._args import address, expect, on_device, stream
-from .wkv7 import OK, WKV7Error, _check, _dtype_code, library
+from .wkv7 import OK, WKV7Error, _check, _dense, _dtype_code, library
 
 
 def _groups(x, params, head_first):
@@ -113,7 +113,7 @@ class LayerNorm(torch.autograd.Function):
     @once_differentiable
     def backward(ctx, dy):
         x, weight, mean, rstd = ctx.saved_tensors
-        r = wkv7_ln_bwd(x, dy.to(x.dtype).contiguous(), mean, rstd, weight,
+        r = wkv7_ln_bwd(x, _dense(dy, x.dtype), mean, rstd, weight,
                         head_first=ctx.head_first,
                         need_params=ctx.needs_input_grad[1] or ctx.needs_input_grad[2])
         dw = r["dweight"] if ctx.needs_input_grad[1] else None

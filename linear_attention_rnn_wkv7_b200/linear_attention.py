@@ -12,7 +12,7 @@ import torch
 from torch.autograd.function import once_differentiable
 
 from ._args import address, expect, on_device, stream
-from .wkv7 import ALGO, OK, WKV7Error, _check, _dtype_code, _head_norm, library
+from .wkv7 import ALGO, OK, WKV7Error, _check, _dense, _dtype_code, _head_norm, library
 
 
 def _sizes(q, k, v, g, s0, mask, cu_seqlens, head_first):
@@ -193,8 +193,8 @@ class DecayLinearAttention(torch.autograd.Function):
     @once_differentiable
     def backward(ctx, do, dsT):
         q, k, v, g, s0, mask, cu_seqlens = ctx.saved_tensors
-        do = torch.zeros_like(v) if do is None else do.to(v.dtype).contiguous()
-        dsT = None if dsT is None else dsT.contiguous().float()
+        do = torch.zeros_like(v) if do is None else _dense(do, v.dtype)
+        dsT = None if dsT is None else _dense(dsT, torch.float32)
         r = wkv7_la_bwd(q, k, v, g, do, s0=s0, mask=mask, dsT=dsT, cu_seqlens=cu_seqlens,
                         scale=ctx.scale, head_first=ctx.head_first,
                         need_dg=ctx.needs_input_grad[3], need_ds0=ctx.needs_input_grad[4])

@@ -137,6 +137,13 @@ def _check(t: torch.Tensor, name: str, dtype=None, shape=None):
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
 
 
+def _dense(t: torch.Tensor, dtype) -> torch.Tensor:
+    """t as the entry points take it: of that type, contiguous, 16-byte aligned.  (The gradient of
+    one of several joined outputs is a view that may begin anywhere.)"""
+    t = t.to(dtype).contiguous()
+    return t if t.data_ptr() % 16 == 0 else t.clone()
+
+
 def _ptr(t):
     return None if t is None else ctypes.c_void_p(t.data_ptr())
 
@@ -446,9 +453,9 @@ class GeneralizedDeltaRule(torch.autograd.Function):
     @staticmethod
     def backward(ctx, do, dsT):
         r, w, k, v, a, b, s0, mask, cu_seqlens = ctx.saved_tensors
-        do = torch.zeros_like(v) if do is None else do.contiguous()
-        dsT = None if dsT is None else dsT.contiguous().float()
-        g = wkv7_bwd(r, w, k, v, a, b, do.to(r.dtype), s0=s0, mask=mask, dsT=dsT,
+        do = torch.zeros_like(v) if do is None else _dense(do, r.dtype)
+        dsT = None if dsT is None else _dense(dsT, torch.float32)
+        g = wkv7_bwd(r, w, k, v, a, b, do, s0=s0, mask=mask, dsT=dsT,
                      cu_seqlens=cu_seqlens, head_first=ctx.head_first)
         ds0 = g["ds0"] if s0 is not None else None
         return g["dr"], g["dw"], g["dk"], g["dv"], g["da"], g["db"], ds0, None, None, None
@@ -611,9 +618,9 @@ class GatedDeltaNet(torch.autograd.Function):
     @staticmethod
     def backward(ctx, do, dsT):
         q, k, v, g, beta, s0, cu_seqlens = ctx.saved_tensors
-        do = torch.zeros_like(v) if do is None else do.contiguous()
-        dsT = None if dsT is None else dsT.contiguous().float()
-        gr = wkv7_gdn_bwd(q, k, v, g, beta, do.to(q.dtype), s0=s0, dsT=dsT,
+        do = torch.zeros_like(v) if do is None else _dense(do, q.dtype)
+        dsT = None if dsT is None else _dense(dsT, torch.float32)
+        gr = wkv7_gdn_bwd(q, k, v, g, beta, do, s0=s0, dsT=dsT,
                           cu_seqlens=cu_seqlens, head_first=ctx.head_first)
         ds0 = gr["ds0"] if s0 is not None else None
         return gr["dq"], gr["dk"], gr["dv"], gr["dg"], gr["dbeta"], ds0, None, None

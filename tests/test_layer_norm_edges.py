@@ -19,3 +19,20 @@ def test_huge_constant_rows_with_idle_lanes(cuda_device, dtype, D, value):
     y, m, r = lib.wkv7_ln_fwd(x, eps=1e-5)
     assert bool((m == value).all()) and bool((y == 0).all())
     assert bool(((r * 1e-5 ** 0.5 - 1).abs() < 1e-6).all())
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("D", [7, 64, 1000])
+def test_gradient_that_is_a_shifted_view(cuda_device, dtype, D):
+    """An output joined behind an odd number of elements gets a dense gradient that is not 16-byte
+    aligned."""
+    gen = torch.Generator().manual_seed(D)
+    x = torch.randn(9, D, generator=gen).to(dtype).cuda().requires_grad_()
+    w, b = (torch.randn(D, generator=gen).cuda().to(dtype).requires_grad_() for _ in range(2))
+    dy = torch.randn(9 * D + 1, generator=gen).to(dtype).cuda()
+    y = lib.layer_norm(x, w, b)
+    want = torch.autograd.grad(y, (x, w, b), dy[1:].clone().view(9, D), retain_graph=True)
+    joined = torch.cat([torch.zeros(1, dtype=dtype, device="cuda"), y.flatten()])
+    got = torch.autograd.grad(joined, (x, w, b), dy)
+    for a, c in zip(got, want):
+        assert torch.equal(a, c)

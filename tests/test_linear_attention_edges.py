@@ -91,3 +91,32 @@ def test_rows_behind_the_last_sequence_are_zero(cuda_device, dtype, D, head_firs
     for n in ("q", "k", "v", "g"):
         assert bool((rows(a[n].grad)[:, end:] == 0).all()), n
     assert lib.wkv7_get_last_error() == OK
+
+
+# ------------------------------------------------------------------- gradients that are views
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("op", ["la", "gdn", "wkv7"])
+def test_gradient_that_is_a_shifted_view(cuda_device, op, dtype):
+    """Outputs joined behind an odd number of elements get gradients that are dense but not
+    16-byte aligned; they give what aligned copies of them give."""
+    gen = torch.Generator().manual_seed(6)
+    B, T, H, D = 1, 70, 2, 64
+    r = lambda *s: torch.randn(*s, generator=gen).to(dtype).cuda()  # noqa: E731
+    q, v = r(B, T, H, D).requires_grad_(), r(B, T, H, D).requires_grad_()
+    k = torch.nn.functional.normalize(r(B, T, H, D).float(), dim=-1).to(dtype)
+    g = -torch.rand(B, T, H, generator=gen).to(dtype).cuda()
+    if op == "la":
+        o, s = lib.decay_linear_attention(q, k, v, g)
+    elif op == "gdn":
+        o, s = lib.gated_delta_net(q, k, v, g, torch.sigmoid(g))
+    else:
+        o, s = lib.generalized_delta_rule(q, g[..., None].expand(B, T, H, D).contiguous(), k, v, -k,
+                                          0.5 * k)
+    do, ds = r(o.numel() + 1), torch.randn(s.numel() + 1, generator=gen).cuda()
+    want = torch.autograd.grad((o, s), (q, v), (do[1:].clone().view_as(o), ds[1:].clone().view_as(s)),
+                               retain_graph=True)
+    one, onef = torch.zeros(1, dtype=dtype, device="cuda"), torch.zeros(1, device="cuda")
+    joined, states = torch.cat([one, o.flatten()]), torch.cat([onef, s.flatten()])
+    got = torch.autograd.grad((joined, states), (q, v), (do, ds))
+    for a, b in zip(got, want):
+        assert torch.equal(a, b)
