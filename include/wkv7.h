@@ -496,7 +496,10 @@ wkv7_status wkv7_la_bwd(const void* q, const void* k, const void* v, const void*
  *   mean, rstd     [rows]        fp32    the statistics that wkv7_ln_bwd takes, or NULL
  *   eps                                  finite, >= 0
  *
- * 1 <= D <= 32768, statistics in fp32 around the mean.
+ * 1 <= D <= 32768, statistics in fp32 around the mean.  mean and rstd need only element
+ * alignment, here and in wkv7_ln_bwd; so do all other tensors but the workspace where a row is no
+ * multiple of 16 bytes (D % 8 for bf16 x, D % 4 for fp32), so that rows of a larger tensor can
+ * be given.
  */
 wkv7_status wkv7_ln_fwd(const void* x, const void* weight, const void* bias, void* y, float* mean,
                         float* rstd, int64_t rows, int groups, int64_t inner, int D, float eps,

@@ -225,6 +225,13 @@ wkv7_status wkv7_test_la_pieces(int B, int T, int H, int K, const int32_t* cu_se
 }
 
 // ---- layer norm -------------------------------------------------------------------------
+// Whether p may hold rows (or weights of rows) of D elements of x's type: such rows are read and
+// written in 16-byte groups where they are whole ones, and else by elements of `type`.
+static bool ln_ptr(const void* p, int D, wkv7_dtype dtype, wkv7_dtype type) {
+    const int group = dtype == WKV7_BF16 ? 8 : 4;
+    return D % group == 0 ? ok_ptr(p) : ok_scalar_ptr(p, type);
+}
+static bool ln_stat_ptr(const float* p) { return !p || ok_scalar_ptr(p, WKV7_F32); }
 static wkv7_status ln_check(long long rows, long long groups, long long inner, long long D,
                             wkv7_dtype dtype, wkv7_dtype wdtype) {
     if (rows < 0 || groups <= 0 || inner <= 0 || D <= 0) return WKV7_ERR_INVALID_ARG;
@@ -246,8 +253,9 @@ wkv7_status wkv7_ln_fwd(const void* x, const void* weight, const void* bias, voi
     if (st != WKV7_OK) return st;
     if (!(eps >= 0.f) || !(eps - eps == 0.f)) return WKV7_ERR_INVALID_ARG;
     if (rows == 0) return WKV7_OK;
-    if (!ok_ptr(x) || !ok_ptr(y) || (weight && !aligned16(weight)) || (bias && !aligned16(bias)) ||
-        !aligned16(mean) || !aligned16(rstd))
+    if (!ln_ptr(x, D, dtype, dtype) || !ln_ptr(y, D, dtype, dtype) ||
+        (weight && !ln_ptr(weight, D, dtype, wdtype)) || (bias && !ln_ptr(bias, D, dtype, wdtype)) ||
+        !ln_stat_ptr(mean) || !ln_stat_ptr(rstd))
         return WKV7_ERR_INVALID_ARG;
     if (one_of(y, x, weight, bias, mean, rstd) || one_of(mean, x, weight, bias, rstd) ||
         one_of(rstd, x, weight, bias))
@@ -280,8 +288,9 @@ wkv7_status wkv7_ln_bwd(const void* x, const void* dy, const float* mean, const 
                         void* workspace, size_t workspace_bytes, void* stream_) {
     const wkv7_status st = ln_check(rows, groups, inner, D, dtype, wdtype);
     if (st != WKV7_OK) return st;
-    if ((weight && !aligned16(weight)) || (dweight && !aligned16(dweight)) ||
-        (dbias && !aligned16(dbias)))
+    if ((weight && !ln_ptr(weight, D, dtype, wdtype)) ||
+        (dweight && !ln_ptr(dweight, D, dtype, wdtype)) ||
+        (dbias && !ln_ptr(dbias, D, dtype, wdtype)))
         return WKV7_ERR_INVALID_ARG;
     cudaStream_t stream = static_cast<cudaStream_t>(stream_);
     if (rows == 0) {
@@ -290,7 +299,8 @@ wkv7_status wkv7_ln_bwd(const void* x, const void* dy, const float* mean, const 
         if (dbias && cudaMemsetAsync(dbias, 0, n, stream) != cudaSuccess) return WKV7_ERR_CUDA;
         return WKV7_OK;
     }
-    if (!ok_ptr(x) || !ok_ptr(dy) || !ok_ptr(dx) || !ok_ptr(mean) || !ok_ptr(rstd))
+    if (!ln_ptr(x, D, dtype, dtype) || !ln_ptr(dy, D, dtype, dtype) || !ln_ptr(dx, D, dtype, dtype) ||
+        !mean || !rstd || !ln_stat_ptr(mean) || !ln_stat_ptr(rstd))
         return WKV7_ERR_INVALID_ARG;
     if (one_of(dx, x, dy, weight, mean, rstd, dweight, dbias) || one_of(dweight, x, dy, weight, dbias) ||
         one_of(dbias, x, dy, weight))

@@ -36,3 +36,24 @@ def test_gradient_that_is_a_shifted_view(cuda_device, dtype, D):
     got = torch.autograd.grad(joined, (x, w, b), dy)
     for a, c in zip(got, want):
         assert torch.equal(a, c)
+
+
+# D a multiple of the 16-byte group: only the statistics may lie anywhere; else every tensor
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("D", [1, 7, 129, 1021, 8193, 64, 4096])
+def test_rows_of_a_larger_tensor(cuda_device, dtype, D):
+    """Rows from the second on: dense, and aligned to an element where a row is no multiple of 16
+    bytes.  They give what the same rows in a tensor of their own give."""
+    gen = torch.Generator().manual_seed(D)
+    x, dy = (torch.randn(6, D, generator=gen).to(dtype).cuda() for _ in range(2))
+    p = torch.randn(2, 1 + D if D % 8 else D, generator=gen).to(dtype).cuda()
+    w, b = (p.flatten()[1:1 + D], p.flatten()[1 + D:1 + 2 * D]) if D % 8 else (p[0], p[1])
+    want, wm, wr = lib.wkv7_ln_fwd(x[1:].clone(), w.clone(), b.clone())
+    out = torch.empty_like(x)
+    y, m, r = lib.wkv7_ln_fwd(x[1:], w, b, y=out[1:])
+    assert torch.equal(y, want) and torch.equal(m, wm) and torch.equal(r, wr)
+    wg = lib.wkv7_ln_bwd(x[1:].clone(), dy[1:].clone(), wm, wr, w.clone())
+    mean, rstd = (torch.cat([t[:1], t]) for t in (wm, wr))
+    g = lib.wkv7_ln_bwd(x[1:], dy[1:], mean[1:], rstd[1:], w)
+    for n in g:
+        assert torch.equal(g[n], wg[n]), n
