@@ -120,3 +120,31 @@ def test_gradient_that_is_a_shifted_view(cuda_device, op, dtype):
     got = torch.autograd.grad((joined, states), (q, v), (do, ds))
     for a, b in zip(got, want):
         assert torch.equal(a, b)
+
+
+# ------------------------------------------------------------- the differentiable op's algorithm
+@pytest.mark.parametrize("D", [64, 128])
+def test_op_takes_the_algorithm(cuda_device, D):
+    """algo reaches both directions: "recurrent" holds all but the results in fp32, so each is off by
+    its own rounding (at most 2^-8 of a value) and fp32's, also where the tensor cores are not."""
+    gen = torch.Generator().manual_seed(D)
+    B, T, H = 2, 200, 3
+    x = {n: torch.randn(B, T, H, D, generator=gen).to(BF16).cuda() for n in ("q", "k", "v", "do")}
+    x["g"] = -torch.rand(B, T, H, generator=gen).to(BF16).cuda() * 0.1
+    want, _ = ref.forward(x["q"], x["k"], x["v"], x["g"], scale=D ** -0.5)
+    size, _ = ref.forward(x["q"], x["k"], x["v"], x["g"], scale=D ** -0.5, absolute=True)
+    results = {}
+    for algo in ("auto", "recurrent"):
+        a = {n: x[n].clone().requires_grad_() for n in ("q", "k", "v", "g")}
+        o, sT = lib.decay_linear_attention(a["q"], a["k"], a["v"], a["g"], scale=D ** -0.5, algo=algo)
+        o.backward(x["do"])
+        fo, fs = lib.wkv7_la_fwd(x["q"], x["k"], x["v"], x["g"], scale=D ** -0.5, algo=algo)
+        # (the op asks for no ds0, and where the state's gradient is no result it is held in fewer bits)
+        r = lib.wkv7_la_bwd(x["q"], x["k"], x["v"], x["g"], x["do"], scale=D ** -0.5, algo=algo,
+                            need_ds0=False)
+        assert torch.equal(o, fo) and torch.equal(sT, fs)
+        for n, t in a.items():
+            assert torch.equal(t.grad, r["d" + n]), n
+        results[algo] = o.detach()
+    ref.check(results["recurrent"], want, ref.allowed(want, size, BF16, T, D, False), "o")
+    assert not torch.equal(results["auto"], results["recurrent"])
