@@ -208,7 +208,7 @@ enum Bar {
     kSReady = 36,  // U0 in bf16 is in shared memory (and the last dU has been read)
     kOut = 37,     // Ox, Oi and every other product of the chunk are done
     kOFree = 38,   // Ox and Oi have been read
-    kDrain = 39,   // after an abort: all MMAs are done
+    kDrain = 39,   // all MMAs are done
     kBars = 40
 };
 
@@ -584,12 +584,12 @@ la_chunked_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constan
                     z_loads = n + 1;
                 }
             }
-            if (!ok) {  // the copies in flight land before the CTA leaves (bounded)
-                for (int m = n < NS ? 0 : n - NS; m < n; ++m)
-                    (void)mbar_wait(cx.bar(kFull + m % NS), (m / NS) & 1);
-                for (int m = z_loads < NS ? 0 : z_loads - NS; m < z_loads; ++m)
-                    (void)mbar_wait(cx.bar(kFullZ + m % NS), (m / NS) & 1);
-            }
+            // The copies in flight land before the CTA leaves (bounded), also when this role is
+            // done and another gives up.
+            for (int m = n < NS ? 0 : n - NS; m < n; ++m)
+                (void)mbar_wait(cx.bar(kFull + m % NS), (m / NS) & 1);
+            for (int m = z_loads < NS ? 0 : z_loads - NS; m < z_loads; ++m)
+                (void)mbar_wait(cx.bar(kFullZ + m % NS), (m / NS) & 1);
         }
     }
     // ------------------------------------------------------------------ warp 1: MMAs
@@ -711,10 +711,9 @@ la_chunked_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constan
                 }
                 if (!have) break;
             }
-            if (!ok) {
-                if (leader) umma_commit(cx.bar(kDrain));
-                (void)mbar_wait(cx.bar(kDrain), 0);
-            }
+            // and so do the MMAs
+            if (leader) umma_commit(cx.bar(kDrain));
+            (void)mbar_wait(cx.bar(kDrain), 0);
         }
     }
     // ------------------------------------------------------------------ warp 2: decays
