@@ -569,6 +569,18 @@ wkv7_status wkv7_test_chunked_schedule(long long units, int len, int* resident, 
                                        long long* cmax);
 
 /*
+ * wkv7_test_hurry_next_la -- test hook of the failure path of the decay linear attention's
+ * tensor-core kernel (no counterpart on the pages), whose waits are bounded as those of the
+ * chunked wkv7_fwd are.  The next wkv7_la_fwd or wkv7_la_bwd that runs that kernel gives each wait
+ * wait_ns nanoseconds instead of a second (plus 20 us for each chunk of the blocks before,
+ * where sequences are cut into equal runs); with handoff_at_once, a block that waits for a state of
+ * the block before gives up at its first look.  Blocks that give up end and leave their
+ * sequences unfinished; wkv7_get_last_error then reports WKV7_ERR_DEVICE_TIMEOUT.
+ * wait_ns = -1 cancels.  Returns WKV7_ERR_INVALID_ARG for wait_ns outside [-1, 10^9].
+ */
+wkv7_status wkv7_test_hurry_next_la(int wait_ns, int handoff_at_once);
+
+/*
  * wkv7_test_la_pieces -- test hook (no counterpart on the pages): the work of block `block`
  * of a pass of the decay linear attention (wkv7_la_fwd; backward = 1: a pass against time),
  * computed on the host by the kernels' own code for a GPU of 148 SMs.  Where sequences are

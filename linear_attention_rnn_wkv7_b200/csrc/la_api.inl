@@ -34,6 +34,17 @@ wkv7_status la_problem(wkv7::la::Problem& p, int B, int T, int H, int K, int V, 
     return WKV7_OK;
 }
 
+// Test hook of the limits on the tensor-core kernel's waits (wkv7_test_hurry_next_la): taken by the
+// next call that runs it.  Bit 31: set; bit 30: handoffs at once; the rest: nanoseconds.
+std::atomic<unsigned> g_hurry{0};
+void take_hurry(wkv7::la::Problem& p) {
+    if (!p.chunked || p.geom.T == 0) return;
+    const unsigned h = g_hurry.exchange(0);
+    if (h == 0) return;
+    p.wait_ns = h & 0x3fffffffu;
+    p.handoff_at_once = (h >> 30) & 1;
+}
+
 // Workspace queries know whether the problem is packed, not where its offsets are: any
 // non-null address makes the same plan.
 const int32_t* la_some_cu(int packed) {
@@ -87,6 +98,7 @@ wkv7_status wkv7_la_fwd(const void* q, const void* k, const void* v, const void*
     if ((long long)N * H == 0) return WKV7_OK;
     cudaStream_t stream = static_cast<cudaStream_t>(stream_);
     uint8_t* ws = static_cast<uint8_t*>(workspace);
+    take_hurry(p);
     auto run = [&](auto zero) {
         using T_ = decltype(zero);
         return wkv7::la::forward<T_>(p, static_cast<const T_*>(q), static_cast<const T_*>(k),
@@ -136,6 +148,7 @@ wkv7_status wkv7_la_bwd(const void* q, const void* k, const void* v, const void*
         return status_of(cudaMemsetAsync(dg, 0, (size_t)H * (p.bf16 ? 2 : 4), stream));
     }
     uint8_t* ws = static_cast<uint8_t*>(workspace);
+    take_hurry(p);
     auto run = [&](auto zero) {
         using T_ = decltype(zero);
         return wkv7::la::backward<T_>(
@@ -194,6 +207,13 @@ wkv7_status wkv7_la_step(const void* q, const void* k, const void* v, const void
                          : wkv7::la::launch_la_step<float>(q, k, v, g, g_per_head != 0, state,
                                                            out_state, o, units, H, K, scale,
                                                            stream));
+}
+
+wkv7_status wkv7_test_hurry_next_la(int wait_ns, int handoff_at_once) {
+    if (wait_ns < -1 || wait_ns > 1000000000) return WKV7_ERR_INVALID_ARG;
+    g_hurry.store(wait_ns < 0 ? 0u
+                              : 1u << 31 | (handoff_at_once ? 1u << 30 : 0u) | (unsigned)wait_ns);
+    return WKV7_OK;
 }
 
 wkv7_status wkv7_test_la_pieces(int B, int T, int H, int K, const int32_t* cu_seqlens, int N,

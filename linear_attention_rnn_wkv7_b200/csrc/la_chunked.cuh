@@ -46,7 +46,7 @@
 // never goes through tensor memory.  All waits are on mbarriers (or a flag in global memory)
 // and bounded; a thread that gives up sets a flag that ends every other wait, so the CTA
 // always reaches its end, waits for its copies and MMAs in flight (bounded), frees its tensor
-// memory and reports WKV7_ERR_DEVICE_TIMEOUT.
+// memory and reports WKV7_ERR_DEVICE_TIMEOUT (tests/test_linear_attention_timeout.py).
 #pragma once
 #include <cuda.h>
 
@@ -263,8 +263,8 @@ struct Ctx {
     }
     __device__ __forceinline__ void arrive(int i) const { mbar_arrive(bar(i)); }
     // The flag of a state handed on, for a whole warp (bounded as the other waits).
-    __device__ __forceinline__ bool wait_handoff(const unsigned* flag) const {
-        return __all_sync(0xffffffffu, handoff_slow(flag, abort, limit));
+    __device__ __forceinline__ bool wait_handoff(const unsigned* flag, int at_once) const {
+        return __all_sync(0xffffffffu, handoff_slow(flag, abort, at_once ? 0 : limit));
     }
 };
 
@@ -486,9 +486,9 @@ la_chunked_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constan
     Ctx cx;
     cx.sbase = smem_u32(smem);
     cx.bars = cx.sbase + C::OFF_BAR;
-    // A second; and for a sequence longer than a run, the CTAs before this one work on it in turn
+    // A second (wait_ns); and for a sequence longer than a run, the CTAs before this one work on it in turn
     // first (20 us for each of their chunks, several times what one takes).
-    cx.limit = 1000000000ull + 20000ull * (uint64_t)p.run * blockIdx.x;
+    cx.limit = p.wait_ns + 20000ull * (uint64_t)p.run * blockIdx.x;
     cx.abort = reinterpret_cast<volatile int*>(smem + C::OFF_BAR + 8 * kBars);
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::OFF_BAR + 8 * kBars + 4);
     if (cx.sbase & 1023u) {  // the swizzled tiles need a 1024-byte aligned base
@@ -1046,7 +1046,8 @@ la_chunked_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constan
             if (has_state) {
                 if (!kStateOnly && p.run > 0 && !wk.begins) {  // handed on by the CTA before
                     const int from = (int)blockIdx.x - 1;
-                    if (!(ok = cx.wait_handoff(p.ho_flag + 8 * from + (sthread >> 5)))) break;
+                    if (!(ok = cx.wait_handoff(p.ho_flag + 8 * from + (sthread >> 5),
+                                               p.handoff_at_once))) break;
                     const float4* src =
                         reinterpret_cast<const float4*>(p.ho_state + (long long)from * D * D) + sthread;
 #pragma unroll

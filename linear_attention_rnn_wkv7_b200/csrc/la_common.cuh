@@ -167,6 +167,8 @@ struct Pass {
     long long dots_stride;
     void* ck;             // states at each chunk's end (layout private to the kernel)
     float* ck_dot;        // [chunk slot][H][parts]: parts of <ck, state before the chunk>
+    unsigned wait_ns;     // limit of a wait of the tensor-core kernel, and (test hook) whether one
+    int handoff_at_once;  // for a state handed on gives up at its first look
 };
 
 // ---- start states of the segments --------------------------------------------------------

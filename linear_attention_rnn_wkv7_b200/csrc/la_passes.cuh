@@ -14,6 +14,8 @@ struct Problem {
     Geom geom;
     int B, D;
     bool bf16, chunked;
+    unsigned wait_ns = 1000000000u;  // a second; less, and the next, by a test hook alone
+    int handoff_at_once = 0;
     long long rows() const { return (long long)B * geom.T * geom.H; }
     // spacing of the states kept for dg
     int ck_every() const { return chunked ? kChunk : kRecChunk; }
@@ -187,6 +189,8 @@ inline cudaError_t forward(const Problem& p, const Tin* q, const Tin* k, const T
     const Handoff ho = carve_handoff(c, p, plan, 1);
     Pass<Tin> a{};
     a.geom = p.geom;
+    a.wait_ns = p.wait_ns;
+    a.handoff_at_once = p.handoff_at_once;
     a.x = q;
     a.y = k;
     a.z = v;
@@ -225,6 +229,8 @@ inline cudaError_t backward(const Problem& p, const Tin* q, const Tin* k, const 
     const BwdSpace b = carve_bwd(p, plan);
     Pass<Tin> f{};  // in the direction of time: dq = A(do, v, k), state S^T
     f.geom = p.geom;
+    f.wait_ns = p.wait_ns;
+    f.handoff_at_once = p.handoff_at_once;
     f.g = g;
     f.g_per_head = g_per_head;
     f.mask = mask;

@@ -100,6 +100,8 @@ def library() -> ctypes.CDLL:
         lib.wkv7_la_zero_tail.argtypes = [p] * 4 + [i, i, i, p, i, i, i, p]
         lib.wkv7_la_step.restype = i
         lib.wkv7_la_step.argtypes = [p] * 4 + [i] + [p] * 3 + [i, i, i, i, f, i, p]
+        lib.wkv7_test_hurry_next_la.restype = i
+        lib.wkv7_test_hurry_next_la.argtypes = [i, i]
         lib.wkv7_test_la_pieces.restype = i
         lib.wkv7_test_la_pieces.argtypes = [i, i, i, i, p, i, i, i, i, p, i, p, p, p]
         lib.wkv7_ln_fwd.restype = i
