@@ -148,3 +148,71 @@ def test_op_takes_the_algorithm(cuda_device, D):
         results[algo] = o.detach()
     ref.check(results["recurrent"], want, ref.allowed(want, size, BF16, T, D, False), "o")
     assert not torch.equal(results["auto"], results["recurrent"])
+
+
+# ------------------------------------------------- results of the state, and long sequences in 64 bits
+def walk_forward(x, scale):
+    """o and the final state in 64 bits, all sequences and heads at once."""
+    S, g = x["s0"].double(), x["g"].double()
+    B, T, H, _ = x["q"].shape
+    g = g.expand(B, T, H) if g.dim() == 1 else g
+    out = []
+    for t in range(T):
+        S = (torch.exp(g[:, t])[..., None, None] * S
+             + x["k"][:, t].double()[..., :, None] * x["v"][:, t].double()[..., None, :])
+        out.append(scale * (x["q"][:, t].double()[..., None, :] @ S)[..., 0, :])
+    return torch.stack(out, 1), S
+
+
+def random_problem(B, T, H, D, gate, seed):
+    gen = torch.Generator().manual_seed(seed)
+    x = {n: torch.randn(B, T, H, D, generator=gen).to(BF16) for n in ("q", "k", "v", "do")}
+    x["k"] = (x["k"].float() / x["k"].float().norm(dim=-1, keepdim=True)).to(BF16)
+    if gate == "token":
+        x["g"] = (-torch.rand(B, T, H, generator=gen) ** 4 * 3.0).to(BF16)
+    else:                               # memories of 32 to 1024 tokens
+        x["g"] = (-torch.exp2(-5 - 5 * torch.rand(H, generator=gen))).to(BF16)
+    x["s0"] = 0.3 * torch.randn(B, H, D, D, generator=gen)
+    x["dsT"] = 0.3 * torch.randn(B, H, D, D, generator=gen)
+    return {n: t.cuda() for n, t in x.items()}
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("gate", ["token", "head"])
+@pytest.mark.parametrize("B,T,H", [(1, 6000, 2), (2, 2000, 64), (40, 300, 4)])
+def test_final_states_need_three_parts(cuda_device, D, gate, B, T, H):
+    """sT (and ds0 below) of the tensor cores: a term's factors are two exponentials, within 2^-22 each,
+    three products and a split in three bf16 parts, half a step of 2^-24 each, and as many
+    decays of half a step as chunks in its memory (8 of these): 2 * 4 + 4 + 8 = 20 half steps if
+    all fell together, 6e-8 * 20 = 1.2e-6.  They do not: 1e-6 in the 2-norm, which the update's
+    operand in two parts (2^-16 of each term, 2.5e-6 here) does not reach."""
+    x = random_problem(B, T, H, D, gate, B + T + D)
+    o, sT = lib.wkv7_la_fwd(x["q"], x["k"], x["v"], x["g"], s0=x["s0"], scale=D ** -0.5)
+    want_o, want_s = walk_forward(x, D ** -0.5)
+    assert float((sT.double() - want_s).norm() / want_s.norm()) <= 1e-6
+    # o: its own rounding, the scores' and the state copy's (each 2^-8 / sqrt(3) / 1.4 at most)
+    assert float((o.double() - want_o).norm() / want_o.norm()) <= 3e-3
+    assert lib.wkv7_get_last_error() == OK
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("gate", ["token", "head"])
+@pytest.mark.parametrize("B,T,H", [(1, 4000, 2), (30, 260, 5)])
+def test_gradients_of_long_sequences(cuda_device, D, gate, B, T, H):
+    """ds0 as sT above; the others are bf16 with the same three roundings as o, dg with those of
+    both products that it is the difference of.  A dg that is summed over batch and tokens may
+    cancel (600 left of terms that add up to 1e5 in magnitude): each token's is off by at most three
+    half steps of the magnitudes that its chunk adds (the scores, the state's copy, the kept
+    state), so the sum by at most three of theirs, and its own rounding."""
+    x = random_problem(B, T, H, D, gate, B + T + D)
+    got = lib.wkv7_la_bwd(x["q"], x["k"], x["v"], x["g"], x["do"], s0=x["s0"], dsT=x["dsT"],
+                          scale=D ** -0.5)
+    args = (x["q"], x["k"], x["v"], x["g"], x["do"], x["s0"], None, x["dsT"], None, D ** -0.5)
+    want = ref.backward(*args)
+    for n, lim in (("dq", 3e-3), ("dk", 3e-3), ("dv", 3e-3), ("dg", 6e-3), ("ds0", 1e-6)):
+        if n == "dg" and gate == "head":
+            size = ref.backward(*args, absolute=True, chunk_sums=True)["dg"]
+            ref.check(got[n], want[n], 3 * ref.U_BF16 * size * (1 + ref.U_BF16) + ref.U_BF16 * want[n].abs(), n)
+            continue
+        assert float((got[n].double() - want[n]).norm() / want[n].norm()) <= lim, n
+    assert lib.wkv7_get_last_error() == OK
