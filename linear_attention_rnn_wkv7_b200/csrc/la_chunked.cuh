@@ -54,6 +54,7 @@
 #include <type_traits>
 
 #include "chunked.cuh"
+#include "f32x2.cuh"
 #include "la_common.cuh"
 #include "sm100.cuh"
 
@@ -133,25 +134,6 @@ __device__ __forceinline__ uint4 ld_shared16(uint32_t addr) {
                  : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
                  : "r"(addr));
     return v;
-}
-// Two fp32 operations in one instruction (a register pair).
-__device__ __forceinline__ uint64_t pair2(float a, float b) {
-    uint64_t r;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
-    return r;
-}
-__device__ __forceinline__ void split2(uint64_t x, float& a, float& b) {
-    asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(x));
-}
-__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
-    uint64_t r;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-    return r;
-}
-__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
-    uint64_t r;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-    return r;
 }
 // The bf16 pair of two fp32, and back.
 __device__ __forceinline__ uint32_t pack2(uint64_t x) {

@@ -22,6 +22,7 @@
 // and dy again by columns.
 #pragma once
 #include "common.cuh"
+#include "f32x2.cuh"
 
 namespace wkv7 {
 namespace ln {
@@ -44,11 +45,6 @@ template <int VEC> __device__ __forceinline__ void load(const float* p, float (&
     if constexpr (VEC == 4) {
         const float4 x = *reinterpret_cast<const float4*>(p);
         v[0] = x.x; v[1] = x.y; v[2] = x.z; v[3] = x.w;
-    } else if constexpr (VEC == 8) {
-        const float4 x = reinterpret_cast<const float4*>(p)[0];
-        const float4 y = reinterpret_cast<const float4*>(p)[1];
-        v[0] = x.x; v[1] = x.y; v[2] = x.z; v[3] = x.w;
-        v[4] = y.x; v[5] = y.y; v[6] = y.z; v[7] = y.w;
     } else {
 #pragma unroll
         for (int i = 0; i < VEC; ++i) v[i] = p[i];
@@ -93,34 +89,14 @@ template <int VEC> __device__ __forceinline__ void store(__nv_bfloat16* p, const
 
 // Pairs of fp32 in one instruction: per element the arithmetic of a row is then half, and HBM
 // and not the issue rate bounds the kernels (forward of 32768 x 4096 bf16: 193 us without).
-__device__ __forceinline__ uint64_t pair2(float a, float b) {
-    uint64_t r;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
-    return r;
-}
-__device__ __forceinline__ void split2(uint64_t x, float& a, float& b) {
-    asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(x));
-}
 __device__ __forceinline__ float sum2(uint64_t x) {
     float a, b;
     split2(x, a, b);
     return a + b;
 }
-__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
-    uint64_t r;
-    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-    return r;
-}
-__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
-    uint64_t r;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-    return r;
-}
-__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
-    uint64_t r;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-    return r;
-}
+using wkv7::add2;
+using wkv7::fma2;
+using wkv7::mul2;
 // A lone value (rows of odd lengths) goes through the same code.
 __device__ __forceinline__ float sum2(float x) { return x; }
 __device__ __forceinline__ float add2(float a, float b) { return a + b; }
@@ -154,7 +130,6 @@ template <int VEC> __device__ __forceinline__ void from_pairs(const Pair<VEC> (&
 // VEC elements as they are in memory (prefetched rows), and as fp32.
 template <typename T, int VEC> struct Raw { T v[VEC]; };
 template <> struct Raw<__nv_bfloat16, 8> { uint4 v; };
-template <> struct Raw<__nv_bfloat16, 4> { uint2 v; };
 template <> struct Raw<float, 8> { float4 v[2]; };
 template <> struct Raw<float, 4> { float4 v; };
 template <typename T, int VEC> __device__ __forceinline__ Raw<T, VEC> load_raw(const T* p) {
