@@ -408,9 +408,11 @@ wkv7_status wkv7_gdn_bwd(const void* q, const void* k, const void* v, const void
  *
  * K == V in {64, 128, 256}.  WKV7_ALGO_CHUNKED: bf16, head sizes 64 and 128, 128-token
  * chunks on tcgen05 tensor cores: scores and states enter its products in bf16, sums, decays
- * and the carried state are fp32 (the state update's operand in two bf16 parts, so sT is as
- * good as fp32's).  Decays need no bound.  WKV7_ALGO_RECURRENT: fp32 on CUDA cores, every
- * type and head size.  AUTO takes the chunked form where it exists.
+ * and the carried state are fp32 (the state update's operand in three bf16 parts where sT is
+ * asked for, so that sT is as good as fp32's, and in two where not).  Decays need no bound (g is
+ * meant to be <= 0; growth is computed as long as e^{its sums over a chunk} fits fp32).
+ * WKV7_ALGO_RECURRENT: fp32 on CUDA cores, every type and head size.  AUTO takes the chunked
+ * form where it exists.
  */
 size_t wkv7_la_fwd_workspace_bytes(int B, int T, int H, int K, int V, int N, int packed,
                                    wkv7_dtype dtype, wkv7_algo algo);

@@ -10,23 +10,29 @@
 //     Oi = P Z     (128 x D, contraction 128)      P read from tensor memory
 //     Ox = X U0    (128 x D, contraction D)        U0 rounded to bf16
 //     dU = (k . Y)^T Z   (D x D, contraction 128, once for each bf16 part of k . Y)
-// Every exponent is a difference over a stretch of tokens, so decays of any strength are
-// exact (nothing is divided by a small prefix).  X, Y, Z enter raw, as TMA left them.
+// Every exponent is a difference over a stretch of tokens, so decays need no bound (nothing is
+// divided by a small prefix).  Inside a 32-token block it is a difference of two prefix sums of
+// the chunk, off by their half steps: 1e-5 of E with ordinary decays, up to 0.4 % (bf16's own half
+// step) behind 100 resets in the same chunk.  X, Y, Z enter raw, as TMA left them.
 //
 // Roundings to bf16: P (as the scores of any attention) and the copy of U0 that Ox reads, each a half
 // step of bf16 of one of the two terms of out.  The state itself is fp32 in registers, and where it
 // is a result (a final state, dS0, a segment's start) its update's operand is split in three
-// bf16 parts (24 bits), so that it is as good as fp32's: with one part it was 2e-3 off, with two
-// 2.5e-6.  Where it only makes bf16 results two parts do.
+// bf16 parts (24 bits), so that it is as good as fp32's: 7e-7 off at most (1.1e-6 in a head whose
+// memory is 4096 tokens), with two parts 2.5e-6, with one 2e-3.  Where it only makes bf16 results
+// two parts do.  In all o and the gradients are 2.34e-3 off in the 2-norm, rounded once 1.66e-3.
 //
 // What bounds it.  At D = 64 a chunk moves 64 KB from and to HBM (1.5 us at an SM's even share)
 // and takes about 1400 cycles of MMA; it takes 2.4 us, because the roles of a chunk
 // (below) each run on one warp per scheduler, at a third of its issue rate: latencies of
 // tensor memory, shared memory and barriers, and instruction fetch (see wait_slow).  At D = 128
 // it takes 4.6 us against 3 us.
-// B = 8, T = 4096, H = 64 of 64: 320 us, 3.4 TB/s, half of the measured copy rate (fp32
-// recurrence 3480 us); 16384 tokens of 16 heads of 128: 141 us with its states made beforehand.
-// The gradients' passes there: 300 us (dv), 430 us (dq, with states kept), 480 us (dk).
+// B = 8, T = 4096, H = 64 of 64: 310 to 336 us from GPU to GPU, 3.3 to 3.5 TB/s, half of the
+// measured copy rate (the recurrence 4.75 ms); 16384 tokens of 16 heads of 128: 137 us with its
+// states made beforehand.  The gradients' passes at the first: 296 us (dv), 440 us (dq, with
+// states kept), 500 us (dk).  All of these move by some percent with where the roles' code falls
+// (310 to 320 and 1250 to 1340 us for forward and backward between builds that differ in cold
+// code only), so small changes want both timed.
 // Tried and left: output staged in a tile of its own (the smaller ring cost as much); rows
 // of the decay scan on all lanes (slower: longer shuffles); waits as calls (each cost the MMA
 // warp 200 cycles more); score blocks of 32 columns (faster alone, slower with all SMs at it).

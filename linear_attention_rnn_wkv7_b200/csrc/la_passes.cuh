@@ -57,7 +57,9 @@ inline Plan make_plan(const Problem& p) {
     const long long all = g.slots(kChunk) * g.H;
     // Whole sequences round robin keep neighbouring heads, whose rows share DRAM pages, at work
     // together: 512 sequences of one length, 3.46 rounds' work in 4 rounds, take 327 us so and
-    // 347 us in runs.  Runs are for what fills its rounds worse, and for packed lengths.
+    // 347 us in runs.  Runs are for what fills its rounds worse, and for packed lengths.  (A
+    // packed sequence longer than a run is worked on by its blocks in turn: 60000 of 69565 tokens
+    // in one of 64 sequences, 32 heads, 970 us, where even lengths take 409 us.)
     const long long rounds = (units + kBlocks - 1) / kBlocks;
     if (p.chunked && !g.cu && units * 5 >= rounds * kBlocks * 4) return best;
     if (p.chunked && units > kBlocks && all <= 0x7fffffffLL) {

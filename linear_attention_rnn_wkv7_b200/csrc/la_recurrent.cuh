@@ -14,8 +14,9 @@
 // read together sit in different banks.
 //
 // fp32, B = 2, T = 333, H = 8 of 64: 115 us in one chain per head (0.34 us a token), 32 us in
-// 32-token segments.  bf16 B = 8, T = 4096, H = 64 here: 3.48 ms, 0.72 ms of it the issue
-// rate's floor.
+// 32-token segments.  B = 8, T = 4096, H = 64 here: bf16 4.75 ms (3.53 ms, and 1.22 ms for its
+// segments' states: the plan cuts it, which does not pay there), fp32 2.96 ms (2.12 + 0.82);
+// 0.72 ms is the issue rate's floor.  Head size 256, 8 x 4096 tokens of 16 heads, bf16: 12.5 ms.
 //
 // Tokens are staged in tiles (fp32, the decay's exponential taken once); the next tile's
 // global loads are in registers while the current one runs.  Outputs leave through
