@@ -40,7 +40,9 @@ struct Plan {
     int run;           // > 0: chunks per block
     long long blocks;  // of the runs
 };
-constexpr int kBlocks = 148;  // SMs
+// SMs of a B200: a plan, and with it the workspace's size, is the same on every device, and a
+// query needs none.  (With fewer SMs runs only take turns: blocks start in order.)
+constexpr int kBlocks = 148;
 
 inline Plan make_plan(const Problem& p) {
     const Geom& g = p.geom;

@@ -216,3 +216,120 @@ def test_gradients_of_long_sequences(cuda_device, D, gate, B, T, H):
             continue
         assert float((got[n].double() - want[n]).norm() / want[n].norm()) <= lim, n
     assert lib.wkv7_get_last_error() == OK
+
+
+# ------------------------------------------------------------------------------ two calls at once
+@pytest.mark.parametrize("kind", ["runs", "packed", "segments"])
+def test_two_calls_at_once(cuda_device, kind):
+    """Forward and backward on two streams at the same time, and rows behind the last sequence too: each
+    call has its own workspace, and its blocks wait for its own blocks alone."""
+    B, T, H, cu = {"runs": (40, 300, 4, None), "segments": (1, 3000, 2, None),
+                   "packed": (1, 6000, 4, [0, 900, 900, 1000] + [1000 + 100 * i for i in range(1, 42)])}[kind]
+    cu_t = None if cu is None else torch.tensor(cu, dtype=torch.int32, device="cuda")
+    N = B if cu is None else len(cu) - 1
+    xs = []
+    for seed in (1, 2):
+        x = random_problem(B, T, H, 64, "token", seed)
+        x["s0"] = torch.randn(N, H, 64, 64, generator=torch.Generator().manual_seed(seed)).cuda()
+        xs.append(x)
+
+    def call(x):
+        o, s = lib.wkv7_la_fwd(x["q"], x["k"], x["v"], x["g"], s0=x["s0"], cu_seqlens=cu_t)
+        r = lib.wkv7_la_bwd(x["q"], x["k"], x["v"], x["g"], x["do"], s0=x["s0"], cu_seqlens=cu_t)
+        return {"o": o, "s": s, **r}
+
+    want = [call(x) for x in xs]
+    streams = [torch.cuda.Stream() for _ in xs]
+    torch.cuda.synchronize()
+    got = [[], []]
+    for _ in range(5):
+        for i, (x, st) in enumerate(zip(xs, streams)):
+            with torch.cuda.stream(st):
+                got[i].append(call(x))
+    torch.cuda.synchronize()
+    for i in range(2):
+        for one in got[i]:
+            for n in one:
+                assert torch.equal(one[n], want[i][n]), (n, i)
+    assert lib.wkv7_get_last_error() == OK
+    for st in streams:
+        with torch.cuda.stream(st):
+            assert lib.wkv7_get_last_error() == OK
+
+
+# -------------------------------------------------- neighbours, states in place, offsets past 32 bits
+@pytest.mark.parametrize("dtype,D", [(F32, 64), (BF16, 64), (BF16, 128)])
+@pytest.mark.parametrize("H", [2, 40])
+def test_gradients_do_not_see_other_sequences(cuda_device, dtype, D, H):
+    """NaN in every row of the other sequences, which share tiles with this one, and behind the last."""
+    gen = torch.Generator().manual_seed(D + H)
+    cu, T = [0, 70, 200, 330, 331, 500], 560
+    N = len(cu) - 1
+    x = {n: torch.randn(1, T, H, D, generator=gen).to(dtype).cuda() for n in ("q", "k", "v", "do")}
+    x["g"] = -torch.rand(1, T, H, generator=gen).to(dtype).cuda()
+    s0, dsT = (torch.randn(N, H, D, D, generator=gen).cuda() for _ in range(2))
+    cu_t = torch.tensor(cu, dtype=torch.int32, device="cuda")
+
+    def call(y, a, b):
+        return lib.wkv7_la_bwd(y["q"], y["k"], y["v"], y["g"], y["do"], s0=a, dsT=b, cu_seqlens=cu_t)
+
+    want = call(x, s0, dsT)
+    for n in range(N):
+        y = {m: torch.full_like(t, float("nan")) for m, t in x.items()}
+        a, b = torch.full_like(s0, float("nan")), torch.full_like(dsT, float("nan"))
+        for m in y:
+            y[m][:, cu[n]:cu[n + 1]] = x[m][:, cu[n]:cu[n + 1]]
+        a[n], b[n] = s0[n], dsT[n]
+        got = call(y, a, b)
+        for m in ("dq", "dk", "dv", "dg"):
+            assert torch.equal(got[m][:, cu[n]:cu[n + 1]], want[m][:, cu[n]:cu[n + 1]]), (m, n)
+            assert bool((got[m][:, cu[-1]:] == 0).all()), m
+        assert torch.equal(got["ds0"][n], want["ds0"][n]), n
+    assert lib.wkv7_get_last_error() == OK
+
+
+@pytest.mark.parametrize("dtype,D", [(F32, 64), (F32, 256), (BF16, 64), (BF16, 128), (BF16, 256)])
+@pytest.mark.parametrize("B,T,H", [(40, 300, 4), (1, 1500, 2), (2, 300, 64)])
+def test_states_in_place(cuda_device, dtype, D, B, T, H):
+    """sT over s0 where sequences are handed from block to block, cut into segments, or neither."""
+    gen = torch.Generator().manual_seed(D + T)
+    q, k, v = (torch.randn(B, T, H, D, generator=gen).to(dtype).cuda() for _ in range(3))
+    g = -torch.rand(B, T, H, generator=gen).to(dtype).cuda() * 0.1
+    s0 = torch.randn(B, H, D, D, generator=gen).cuda()
+    o, sT = lib.wkv7_la_fwd(q, k, v, g, s0=s0)
+    for _ in range(3):
+        s = s0.clone()
+        o2, s2 = lib.wkv7_la_fwd(q, k, v, g, s0=s, sT=s)
+        assert s2.data_ptr() == s.data_ptr() and torch.equal(o, o2) and torch.equal(sT, s)
+
+
+def test_more_elements_than_32_bits_count(cuda_device):
+    """2.28e9 elements a tensor: the last batch row's results are those of a call of its own (cut
+    differently: each is off by bf16's roundings of its terms), forward, backward and layer norm."""
+    B, T, H, D = 34, 8192, 64, 128
+    gen = torch.Generator(device="cuda").manual_seed(1)
+    x = {n: torch.randn(B, T, H, D, device="cuda", generator=gen, dtype=BF16) for n in ("q", "k", "v", "do")}
+    assert x["q"].numel() > 2 ** 31
+    x["k"] *= D ** -0.5
+    x["g"] = (-torch.rand(B, T, H, device="cuda", generator=gen) * 0.2).to(BF16)
+    last = {n: t[-1:].clone() for n, t in x.items()}
+
+    def rel(a, b):
+        return float((a.double() - b.double()).norm() / b.double().norm())
+
+    o, s = lib.wkv7_la_fwd(x["q"], x["k"], x["v"], x["g"], scale=D ** -0.5)
+    lo, ls = lib.wkv7_la_fwd(last["q"], last["k"], last["v"], last["g"], scale=D ** -0.5)
+    # two results that are each within 3e-3 (states 1e-6) of the definition
+    assert rel(o[-1:], lo) <= 6e-3 and rel(s[-1:], ls) <= 2e-6
+    y, m, r = lib.wkv7_ln_fwd(o)
+    ly, lm, lr = lib.wkv7_ln_fwd(o[-1:].clone())
+    assert torch.equal(y[-1:], ly) and torch.equal(m[-1:], lm) and torch.equal(r[-1:], lr)
+    del y
+    gx = lib.wkv7_ln_bwd(o, x["do"], m, r)["dx"]
+    assert torch.equal(gx[-1:], lib.wkv7_ln_bwd(o[-1:].clone(), last["do"], lm, lr)["dx"])
+    del gx, o
+    b = lib.wkv7_la_bwd(x["q"], x["k"], x["v"], x["g"], x["do"], scale=D ** -0.5)
+    lb = lib.wkv7_la_bwd(last["q"], last["k"], last["v"], last["g"], last["do"], scale=D ** -0.5)
+    for n in ("dq", "dk", "dv", "dg", "ds0"):
+        assert rel(b[n][-1:], lb[n]) <= (2e-6 if n == "ds0" else 1.2e-2 if n == "dg" else 6e-3), n
+    assert lib.wkv7_get_last_error() == OK
